@@ -459,7 +459,7 @@ def _library(s):
         out = dict(y=f["y"], final_state=f["final_state"])
         if train:
             b = layers.selective_scan_bwd(s["x"], s["dt"], s["A"], s["B"], s["C"], f["states"], s["dy"], skip=s["skip"],
-                                          z=s["z"], dt_bias=s["dt_bias"], dfinal=s["dfinal"], cu_seqlens=pack,
+                                          z=s["z"], dt_bias=s["dt_bias"], dfinal=s["dfinal"], **packed,
                                           dt_softplus=True, output_dh0=s["h0"] is not None)
             names = ["dx", "ddt", "ddt_bias", "dA", "dskip", "dB", "dC"]
             names += ["dz"] if s["z"] is not None else []
