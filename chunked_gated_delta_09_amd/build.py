@@ -16,6 +16,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libkda.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["kda_api.cpp", "kda_fwd.hip", "kda_scan.hip", "kda_bwd.hip", "kda_noalloc.hip"]
+# the operators around the chunk recurrence (include/kda_layers.h): no matrix products among them
+LAYER_SOURCES = ["layer_api.cpp", "layer_conv.hip", "layer_sscan.hip", "layer_norm.hip", "layer_step.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 VALU instructions are disabled: plain float code is compiled to scalar VALU ops.
@@ -45,8 +47,8 @@ def _compile(src: str) -> str:
 def build(verbose: bool = False) -> str:
     """Compile every source and link libkda.so next to this file. Always rebuilds."""
     os.makedirs(OBJDIR, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(_compile, SOURCES))
+    with concurrent.futures.ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as ex:
+        objs = list(ex.map(_compile, SOURCES + LAYER_SOURCES))
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", "-mcode-object-version=5", "-o", tmp] + objs
     res = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,0 +1,460 @@
+// Short causal convolution: forward, backward and single-token step.
+//
+// A thread owns VEC neighbouring channels and walks a run of tokens with the last W - 1 inputs in
+// registers, so every input is loaded once per run plus W - 1 rows in front of it. The work is
+// bound by memory; the multiplications are a few per element.
+#include "layer_device.h"
+
+namespace kda {
+
+namespace {
+
+// Tokens whose loads are issued together.
+constexpr int kAhead = 8;
+
+struct Cursor {
+  int n;               // sequence of the current token
+  int64_t begin, end;  // its tokens
+};
+
+__device__ __forceinline__ Cursor cursor_at(const Seqs& s, int64_t t) {
+  Cursor c;
+  c.n = seq_of(s, t);
+  c.begin = seq_begin(s, c.n);
+  c.end = seq_end(s, c.n);
+  return c;
+}
+// The next sequence that has a token (the caller's token t is one).
+__device__ __forceinline__ void advance(const Seqs& s, Cursor& c, int64_t t) {
+  while (t >= c.end) {
+    ++c.n;
+    c.begin = c.end;
+    c.end = seq_end(s, c.n);
+  }
+}
+
+// Row r of a sequence's history [h0 | tokens] (r < W - 1: h0), for `ch` and VEC - 1 channels behind it.
+template <class T, int W, int VEC>
+__device__ __forceinline__ void history_row(const ConvArgs& a, int n, int64_t begin, int64_t r, int ch, int valid,
+                                            float (&out)[VEC]) {
+  if (r >= W - 1) {
+    const auto v = load_n<T, VEC>(static_cast<const T*>(a.x) + (begin + r - (W - 1)) * a.x_row + ch, valid, VEC > 1);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) out[e] = as_f(v.v[e]);
+  } else if (a.h0 != nullptr) {
+    const auto v = load_n<T, VEC>(static_cast<const T*>(a.h0) + ((int64_t)n * (W - 1) + r) * a.D + ch, valid, VEC > 1);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) out[e] = as_f(v.v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) out[e] = 0.f;
+  }
+}
+
+template <int W, int VEC>
+__device__ __forceinline__ void load_filter(const ConvArgs& a, int ch, float (&w)[W][VEC], float (&b)[VEC]) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    const bool in = ch + e < a.D;
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][e] = in ? a.w[(int64_t)(ch + e) * W + j] : 0.f;
+    b[e] = in && a.bias != nullptr ? a.bias[ch + e] : 0.f;
+  }
+}
+
+// Grid: (token runs, then the sequences' final states) x channel blocks. Block: cx channel
+// threads x (256 / cx) runs.
+template <class T, int W, int VEC>
+__global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int cx, int64_t run_blocks) {
+  const int tx = threadIdx.x % cx, ty = threadIdx.x / cx, rows = 256 / cx;
+  const int64_t rb = blockIdx.x;
+  const int ch = (blockIdx.y * cx + tx) * VEC;
+  const int valid = a.D - ch;
+  if (valid <= 0) return;
+  if (rb >= run_blocks) {  // final state of `rows` sequences a block
+    const int64_t n = (rb - run_blocks) * rows + ty;
+    if (n >= a.sq.n) return;
+    const int64_t begin = seq_begin(a.sq, (int)n), len = seq_end(a.sq, (int)n) - begin;
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) {
+      float v[VEC];
+      history_row<T, W, VEC>(a, (int)n, begin, len + i, ch, valid, v);
+      store_n<T, VEC>(static_cast<T*>(a.final_state) + (n * (W - 1) + i) * a.D + ch, v, valid, VEC > 1);
+    }
+    return;
+  }
+  const int64_t t0 = (rb * rows + ty) * a.tt;
+  if (t0 >= a.sq.total) return;
+  const int64_t t1 = min(t0 + a.tt, a.sq.total);
+  float w[W][VEC], b[VEC], win[W][VEC];  // win[j]: the input of tap j
+  load_filter<W, VEC>(a, ch, w, b);
+  Cursor c = cursor_at(a.sq, t0);
+#pragma unroll
+  for (int j = 1; j < W; ++j) history_row<T, W, VEC>(a, c.n, c.begin, t0 - c.begin + j - 1, ch, valid, win[j]);
+  const T* x = static_cast<const T*>(a.x);
+  T* y = static_cast<T*>(a.y);
+  for (int64_t t = t0; t < t1; t += kAhead) {
+    Vec<T, VEC> in[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (t + i < t1) in[i] = load_n<T, VEC>(x + (t + i) * a.x_row + ch, valid, VEC > 1);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (t + i < t1) {
+        if (t + i >= c.end) {
+          advance(a.sq, c, t + i);
+#pragma unroll
+          for (int j = 1; j < W; ++j) history_row<T, W, VEC>(a, c.n, c.begin, j - 1, ch, valid, win[j]);
+        }
+        float out[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j) win[j][e] = win[j + 1][e];
+          win[W - 1][e] = as_f(in[i].v[e]);
+          float u = b[e];
+#pragma unroll
+          for (int j = 0; j < W; ++j) u = fmaf(w[j][e], win[j][e], u);
+          out[e] = a.act ? u * sigmoid(u) : u;
+        }
+        store_n<T, VEC>(y + (t + i) * a.D + ch, out, valid, VEC > 1);
+      }
+    }
+  }
+}
+
+// Backward of a run [t0, t1): du_t = dy_t act'(u_t) for its tokens and the W - 1 behind them (of
+// their sequence), each added into the pending dx of the W tokens that it saw; dx of a token is
+// whole once du of the token W - 1 behind it is in. The filter's gradient is summed over the run
+// in registers, over the block's runs in shared memory, and over blocks by a second kernel: one
+// fixed order, no atomics.
+template <class T, int W, int VEC>
+__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int cx, int64_t run_blocks) {
+  extern __shared__ float sh[];  // [rows][W + 1][cx * VEC]
+  const int tx = threadIdx.x % cx, ty = threadIdx.x / cx, rows = 256 / cx;
+  const int64_t rb = blockIdx.x;
+  const int ch = (blockIdx.y * cx + tx) * VEC;
+  const int valid = a.D - ch;
+  const T* x = static_cast<const T*>(a.x);
+  const T* dy = static_cast<const T*>(a.dy);
+  float w[W][VEC], b[VEC];
+  if (valid > 0) load_filter<W, VEC>(a, ch, w, b);
+  if (rb >= run_blocks) {  // dh0 of `rows` sequences a block: history rows 0 .. W - 2
+    const int64_t n = (rb - run_blocks) * rows + ty;
+    if (n >= a.sq.n || valid <= 0) return;
+    const int64_t begin = seq_begin(a.sq, (int)n), len = seq_end(a.sq, (int)n) - begin;
+    float acc[W - 1][VEC], win[W][VEC];
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[i][e] = 0.f;
+      history_row<T, W, VEC>(a, (int)n, begin, i, ch, valid, win[i + 1]);
+      if (a.dfinal != nullptr && i >= len) {
+        const auto d = load_n<T, VEC>(static_cast<const T*>(a.dfinal) + (n * (W - 1) + i - len) * a.D + ch, valid, VEC > 1);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[i][e] = as_f(d.v[e]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < W - 1; ++t) {
+      if (t < len) {
+        const auto in = load_n<T, VEC>(x + (begin + t) * a.x_row + ch, valid, VEC > 1);
+        const auto g = load_n<T, VEC>(dy + (begin + t) * a.D + ch, valid, VEC > 1);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j) win[j][e] = win[j + 1][e];
+          win[W - 1][e] = as_f(in.v[e]);
+          float u = b[e];
+#pragma unroll
+          for (int j = 0; j < W; ++j) u = fmaf(w[j][e], win[j][e], u);
+          const float du = as_f(g.v[e]) * (a.act ? dact_f(u, KDA_ACT_SILU) : 1.f);
+#pragma unroll
+          for (int j = 0; j < W; ++j)
+            if (t + j < W - 1) acc[t + j][e] = fmaf(w[j][e], du, acc[t + j][e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i)
+      store_n<T, VEC>(static_cast<T*>(a.dh0) + (n * (W - 1) + i) * a.D + ch, acc[i], valid, VEC > 1);
+    return;
+  }
+  const int64_t t0 = (rb * rows + ty) * a.tt;
+  float dw[W][VEC], db[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    db[e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) dw[j][e] = 0.f;
+  }
+  if (valid > 0 && t0 < a.sq.total) {
+    const int64_t t1 = min(t0 + a.tt, a.sq.total);
+    float win[W][VEC], pend[W][VEC];  // pend[m]: dx so far of the token W - 1 - m before the current one
+    Cursor c = cursor_at(a.sq, t0);
+#pragma unroll
+    for (int j = 1; j < W; ++j) history_row<T, W, VEC>(a, c.n, c.begin, t0 - c.begin + j - 1, ch, valid, win[j]);
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) pend[j][e] = 0.f;
+    // what dfinal adds to dx of token s: rows len .. len + W - 2 of the history are the final state
+    auto finish = [&](int64_t s, float (&v)[VEC]) {
+      if (a.dfinal != nullptr) {
+        Cursor f = s >= c.begin ? c : cursor_at(a.sq, s);
+        const int64_t i = (W - 1) - (f.end - s);
+        if (i >= 0) {
+          const auto d = load_n<T, VEC>(static_cast<const T*>(a.dfinal) + ((int64_t)f.n * (W - 1) + i) * a.D + ch, valid, VEC > 1);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) v[e] += as_f(d.v[e]);
+        }
+      }
+      store_n<T, VEC>(static_cast<T*>(a.dx) + s * a.D + ch, v, valid, VEC > 1);
+    };
+    const int64_t t2 = min(t1 + W - 1, a.sq.total);
+    for (int64_t t = t0; t < t1 + W - 1; t += kAhead) {
+      Vec<T, VEC> in[kAhead], g[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (t + i < t2) {
+          in[i] = load_n<T, VEC>(x + (t + i) * a.x_row + ch, valid, VEC > 1);
+          g[i] = load_n<T, VEC>(dy + (t + i) * a.D + ch, valid, VEC > 1);
+        }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t s = t + i;
+        if (s < t1 + W - 1) {
+          if (s < t2) {
+            if (s >= c.end) {
+              advance(a.sq, c, s);
+#pragma unroll
+              for (int j = 1; j < W; ++j) history_row<T, W, VEC>(a, c.n, c.begin, j - 1, ch, valid, win[j]);
+            }
+            const int64_t pos = s - c.begin;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+              for (int j = 0; j < W - 1; ++j) {
+                win[j][e] = win[j + 1][e];
+                pend[j][e] = pend[j + 1][e];
+              }
+              win[W - 1][e] = as_f(in[i].v[e]);
+              pend[W - 1][e] = 0.f;
+              float u = b[e];
+#pragma unroll
+              for (int j = 0; j < W; ++j) u = fmaf(w[j][e], win[j][e], u);
+              const float du = as_f(g[i].v[e]) * (a.act ? dact_f(u, KDA_ACT_SILU) : 1.f);
+#pragma unroll
+              for (int j = 0; j < W; ++j)
+                if (pos >= W - 1 - j) pend[j][e] = fmaf(w[j][e], du, pend[j][e]);
+              if (s < t1) {
+                db[e] += du;
+#pragma unroll
+                for (int j = 0; j < W; ++j) dw[j][e] = fmaf(du, win[j][e], dw[j][e]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+              for (int j = 0; j < W - 1; ++j) pend[j][e] = pend[j + 1][e];
+              pend[W - 1][e] = 0.f;
+            }
+          }
+          if (s - (W - 1) >= t0 && s - (W - 1) < t1) finish(s - (W - 1), pend[0]);
+        }
+      }
+    }
+  }
+  // [rows][W + 1][cx * VEC] -> one row of partial sums a block
+  const int width = cx * VEC;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) sh[(ty * (W + 1) + j) * width + tx * VEC + e] = dw[j][e];
+    sh[(ty * (W + 1) + W) * width + tx * VEC + e] = db[e];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < (W + 1) * width; i += 256) {
+    const int j = i / width, col = blockIdx.y * width + i % width;
+    float s = 0.f;
+    for (int r = 0; r < rows; ++r) s += sh[(r * (W + 1) + j) * width + i % width];
+    if (col < a.D) a.part[((int64_t)rb * (W + 1) + j) * a.D + col] = s;
+  }
+}
+
+// dweight [D][W] and dbias [D] from [blocks][W + 1][D]; 64 columns a workgroup, the blocks' rows
+// dealt to 16 lanes a column and joined in order.
+template <int W>
+__global__ __launch_bounds__(1024) void conv_filter_kernel(ConvArgs a, int64_t blocks) {
+  __shared__ float sh[16][65];
+  const int cols = (W + 1) * a.D;
+  const int tx = threadIdx.x % 64, ty = threadIdx.x / 64;
+  const int col = blockIdx.x * 64 + tx;
+  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+  if (col < cols) {
+    int64_t r = ty;
+    for (; r + 48 < blocks; r += 64) {
+      s0 += a.part[r * cols + col];
+      s1 += a.part[(r + 16) * cols + col];
+      s2 += a.part[(r + 32) * cols + col];
+      s3 += a.part[(r + 48) * cols + col];
+    }
+    for (; r < blocks; r += 16) s0 += a.part[r * cols + col];
+  }
+  sh[ty][tx] = (s0 + s1) + (s2 + s3);
+  __syncthreads();
+  if (ty == 0 && col < cols) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += sh[i][tx];
+    const int j = col / a.D, ch = col % a.D;
+    if (j < W) a.dw[(int64_t)ch * W + j] = s;
+    else if (a.db != nullptr) a.db[ch] = s;
+  }
+}
+
+template <class T, int W, int VEC>
+__global__ __launch_bounds__(256) void conv_step_kernel(ConvStepArgs a) {
+  const int b = blockIdx.y;
+  const int ch = (blockIdx.x * 256 + threadIdx.x) * VEC;
+  const int slot = step_slot(a.slots, b, a.slots_n);
+  const int valid = a.D - ch;
+  if (valid <= 0) return;
+  T* y = static_cast<T*>(a.y) + (int64_t)b * a.D + ch;
+  float out[VEC];
+  if (slot < 0) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) out[e] = slot == -1 ? 0.f : __builtin_nanf("");
+    store_n<T, VEC>(y, out, valid, VEC > 1);
+    return;
+  }
+  T* st = static_cast<T*>(a.state) + (int64_t)slot * (W - 1) * a.D + ch;
+  Vec<T, VEC> old[W - 1];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) old[j] = load_n<T, VEC>(st + (int64_t)j * a.D, valid, VEC > 1);
+  const auto x = load_n<T, VEC>(static_cast<const T*>(a.x) + b * a.x_row + ch, valid, VEC > 1);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    const bool in = e < valid;
+    float u = in && a.bias != nullptr ? a.bias[ch + e] : 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      u = fmaf(in ? a.w[(int64_t)(ch + e) * W + j] : 0.f, as_f(j < W - 1 ? old[j < W - 1 ? j : 0].v[e] : x.v[e]), u);
+    out[e] = a.act ? u * sigmoid(u) : u;
+  }
+  store_n<T, VEC>(y, out, valid, VEC > 1);
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) {
+    float v[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = as_f(j + 1 < W - 1 ? old[j + 1 < W - 1 ? j + 1 : 0].v[e] : x.v[e]);
+    store_n<T, VEC>(st + (int64_t)j * a.D, v, valid, VEC > 1);
+  }
+}
+
+// Channel threads of a block: the power of two that covers the channels, up to `most`.
+int channel_threads(int D, int vec, int most) {
+  int cx = 1;
+  while (cx < most && cx * vec < D) cx *= 2;
+  return cx;
+}
+
+template <class T, int W>
+hipError_t fwd_w(const ConvArgs& a, hipStream_t st) {
+  const int cx = channel_threads(a.D, a.vec, 256), rows = 256 / cx;
+  const int64_t runs = (a.sq.total + a.tt - 1) / a.tt, rb = (runs + rows - 1) / rows;
+  const int64_t fb = a.final_state != nullptr ? (a.sq.n + rows - 1) / rows : 0;
+  if (rb + fb == 0) return hipSuccess;
+  const dim3 grid((unsigned)(rb + fb), (a.D + cx * a.vec - 1) / (cx * a.vec));
+  if constexpr (sizeof(T) == 2)
+    if (a.vec == 8) {
+      hipLaunchKernelGGL((conv_fwd_kernel<T, W, 8>), grid, dim3(256), 0, st, a, cx, rb);
+      return hipGetLastError();
+    }
+  if (a.vec == 4)
+    hipLaunchKernelGGL((conv_fwd_kernel<T, W, 4>), grid, dim3(256), 0, st, a, cx, rb);
+  else
+    hipLaunchKernelGGL((conv_fwd_kernel<T, W, 1>), grid, dim3(256), 0, st, a, cx, rb);
+  return hipGetLastError();
+}
+
+template <class T, int W>
+hipError_t bwd_w(const ConvArgs& a, hipStream_t st) {
+  const int vec = a.vec > 1 ? 4 : 1;
+  const int cx = channel_threads(a.D, vec, 64), rows = 256 / cx;
+  const int64_t rb = conv_row_blocks(a);
+  const int64_t hb = a.dh0 != nullptr ? (a.sq.n + rows - 1) / rows : 0;
+  const size_t lds = sizeof(float) * 256 * vec * (W + 1);
+  const dim3 grid((unsigned)(rb + hb), (a.D + cx * vec - 1) / (cx * vec));
+  if (rb + hb > 0) {
+    if (vec == 4)
+      hipLaunchKernelGGL((conv_bwd_kernel<T, W, 4>), grid, dim3(256), lds, st, a, cx, rb);
+    else
+      hipLaunchKernelGGL((conv_bwd_kernel<T, W, 1>), grid, dim3(256), lds, st, a, cx, rb);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((conv_filter_kernel<W>), dim3(((W + 1) * a.D + 63) / 64), dim3(1024), 0, st, a, rb);
+  return hipGetLastError();
+}
+
+template <class T, int W>
+hipError_t step_w(const ConvStepArgs& a, hipStream_t st) {
+  const void* p[3] = {a.x, a.state, a.y};
+  const int vec = conv_vec(sizeof(T) == 4 ? KDA_F32 : KDA_BF16, a.D, a.x_row, p, 3) > 1 ? 4 : 1;
+  const dim3 grid((a.D + 256 * vec - 1) / (256 * vec), a.B);
+  if (vec == 4)
+    hipLaunchKernelGGL((conv_step_kernel<T, W, 4>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((conv_step_kernel<T, W, 1>), grid, dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+#define CONV_DISPATCH(FN, A)                                             \
+  do {                                                                   \
+    if (dtype == KDA_F32) {                                              \
+      if ((A).W == 2) return FN<float, 2>(A, st);                        \
+      if ((A).W == 3) return FN<float, 3>(A, st);                        \
+      return FN<float, 4>(A, st);                                        \
+    }                                                                    \
+    if ((A).W == 2) return FN<bf16, 2>(A, st);                           \
+    if ((A).W == 3) return FN<bf16, 3>(A, st);                           \
+    return FN<bf16, 4>(A, st);                                           \
+  } while (0)
+
+}  // namespace
+
+// Channels of a thread: 16 bytes a load where every row starts on a multiple of them, half of it
+// for bf16 rows that only allow that, single elements otherwise.
+int conv_vec(int dtype, int D, int64_t x_row, const void* const* ptrs, int np) {
+  const int es = dtype == KDA_F32 ? 4 : 2;
+  for (int vec = 16 / es; vec >= 4; vec /= 2) {
+    bool ok = D % vec == 0 && x_row % vec == 0;
+    for (int i = 0; i < np; ++i) ok = ok && reinterpret_cast<uintptr_t>(ptrs[i]) % (vec * es) == 0;
+    if (ok) return vec;
+  }
+  return 1;
+}
+
+// Tokens of a run: as many as leave about 2048 waves, from 8 to 32 (a longer run reads its W - 1
+// rows in front less often, a shorter one gives more waves to a small call).
+int conv_tile(int64_t total, int D, int vec) {
+  const int64_t cols = (D + vec - 1) / vec;
+  int tt = 32;
+  while (tt > 8 && (total + tt - 1) / tt * cols < 2048 * 64) tt /= 2;
+  return tt;
+}
+
+int64_t conv_row_blocks(const ConvArgs& a) {
+  const int vec = a.vec > 1 ? 4 : 1;
+  const int rows = 256 / channel_threads(a.D, vec, 64);
+  const int64_t runs = (a.sq.total + a.tt - 1) / a.tt;
+  return (runs + rows - 1) / rows;
+}
+
+hipError_t launch_conv_fwd(int dtype, const ConvArgs& a, hipStream_t st) { CONV_DISPATCH(fwd_w, a); }
+hipError_t launch_conv_bwd(int dtype, const ConvArgs& a, hipStream_t st) { CONV_DISPATCH(bwd_w, a); }
+hipError_t launch_conv_step(int dtype, const ConvStepArgs& a, hipStream_t st) { CONV_DISPATCH(step_w, a); }
+
+}  // namespace kda

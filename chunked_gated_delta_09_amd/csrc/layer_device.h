@@ -1,0 +1,126 @@
+// Device-side helpers shared by the layer operators' kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "layer_launch.h"
+
+namespace kda {
+
+typedef __bf16 bf16;
+
+template <class T, int N>
+struct alignas(sizeof(T) * N) Vec {
+  T v[N];
+};
+
+__device__ __forceinline__ float as_f(bf16 x) { return (float)x; }
+__device__ __forceinline__ float as_f(float x) { return x; }
+
+// N elements at p, as floats; lanes take those below `valid`, zero behind. `vec`: p is aligned
+// for one load of all N.
+template <class T, int N>
+__device__ __forceinline__ Vec<T, N> load_n(const T* p, int valid, bool vec) {
+  Vec<T, N> r;
+  if (vec && valid >= N) {
+    r = *reinterpret_cast<const Vec<T, N>*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.v[i] = i < valid ? p[i] : (T)0.f;
+  }
+  return r;
+}
+
+template <class T, int N>
+__device__ __forceinline__ void store_n(T* p, const float (&x)[N], int valid, bool vec) {
+  if (vec && valid >= N) {
+    Vec<T, N> r;
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.v[i] = (T)x[i];
+    *reinterpret_cast<Vec<T, N>*>(p) = r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < valid) p[i] = (T)x[i];
+  }
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x by the hardware instruction (results below the normal range become zero).
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+// 1 / (1 + e^-x): e^-x overflows to infinity for x < -88.7, where the quotient is zero as it should be.
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + exp2_hw(-kLog2e * x)); }
+// log(1 + e^x) = max(x, 0) + log1p(e^-|x|): no overflow, and full relative precision for very
+// negative x, where it is e^x. log1p(e) with u = 1 + e rounded is log(u) + (e - (u - 1)) / u.
+__device__ __forceinline__ float softplus(float x) {
+  const float e = exp2_hw(-kLog2e * fabsf(x));
+  const float u = 1.f + e;
+  return fmaxf(x, 0.f) + (__logf(u) + (e - (u - 1.f)) * __builtin_amdgcn_rcpf(u));
+}
+
+// y = act(x) and its derivative for kda_act codes.
+__device__ __forceinline__ float act_f(float x, int act) {
+  if (act == KDA_ACT_NONE) return x;
+  const float s = sigmoid(x);
+  return act == KDA_ACT_SIGMOID ? s : x * s;
+}
+__device__ __forceinline__ float dact_f(float x, int act) {
+  if (act == KDA_ACT_NONE) return 1.f;
+  const float s = sigmoid(x);
+  return act == KDA_ACT_SIGMOID ? s * (1.f - s) : s * (1.f + x * (1.f - s));
+}
+
+// Value of the lane whose number differs by the power of two D.
+template <int D>
+__device__ __forceinline__ float xor_lane(float x) {
+  const int v = __float_as_int(x);
+  if constexpr (D == 1) return __int_as_float(__builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true));  // quad_perm 1,0,3,2
+  if constexpr (D == 2) return __int_as_float(__builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true));  // quad_perm 2,3,0,1
+  if constexpr (D > 2) return __shfl_xor(x, D, 64);
+}
+
+// Sum over the L lanes of an aligned group (L a power of two).
+template <int L>
+__device__ __forceinline__ float group_sum(float x) {
+  if constexpr (L >= 2) x += xor_lane<1>(x);
+  if constexpr (L >= 4) x += xor_lane<2>(x);
+  if constexpr (L >= 8) x += xor_lane<4>(x);
+  if constexpr (L >= 16) x += xor_lane<8>(x);
+  if constexpr (L >= 32) x += xor_lane<16>(x);
+  if constexpr (L >= 64) x += xor_lane<32>(x);
+  return x;
+}
+
+// The sequence that holds token t: the last n with first(n) <= t, over a table of n + 1 firsts.
+__device__ __forceinline__ int find_seq(const int32_t* first, int n, int64_t t) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ int64_t seq_begin(const Seqs& s, int n) { return s.cu ? s.cu[n] : (int64_t)n * s.T; }
+__device__ __forceinline__ int64_t seq_end(const Seqs& s, int n) { return s.cu ? s.cu[n + 1] : (int64_t)(n + 1) * s.T; }
+__device__ __forceinline__ int seq_of(const Seqs& s, int64_t t) {
+  return s.cu ? find_seq(s.cu, s.n, t) : (int)(t / s.T);
+}
+
+// The state row of batch row b in a token step: slots[b], or b itself without a table. A negative slot
+// is a padding row (-1); a slot behind the last row, or one that an earlier batch row has already, is
+// refused (-2): the first batch row owns it, and two rows never write the same state. The whole
+// workgroup calls it.
+__device__ __forceinline__ int step_slot(const int32_t* slots, int b, int n) {
+  if (slots == nullptr) return b;
+  const int s = slots[b];
+  int seen = 0;
+  for (int i = threadIdx.x; i < b; i += blockDim.x) seen |= slots[i] == s;
+  seen = __syncthreads_or(seen);
+  if (s < 0) return -1;
+  return s >= n || seen ? -2 : s;
+}
+
+}  // namespace kda
