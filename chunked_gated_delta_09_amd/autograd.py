@@ -10,12 +10,14 @@ entirely in the HIP library; this module only marshals tensors (FLA chunk_bwd pa
 `chunk_kda_bwd` takes the forward's saved inverses and states and returns dq, dk, dv,
 dbeta, dg, dh0; FlashKDA backward page: the chunk kernel's inputs are the forward
 workspace and dO).
+
+`short_conv`, `selective_scan` and `group_norm` are the operators of ``layers`` in the same form.
 """
 from __future__ import annotations
 
 import torch
 
-from . import chunk_bwd, fwd_states
+from . import chunk_bwd, fwd_states, layers
 
 
 class KdaChunkFunction(torch.autograd.Function):
@@ -55,3 +57,84 @@ def kda_chunk(q, k, v, g, beta, h0=None, cu_seqlens=None, C=64, scale=None, outp
     [N,HV,K,V] fp32 or None)."""
     return KdaChunkFunction.apply(q, k, v, g, beta, h0, cu_seqlens, C, scale, output_final_state, beta_logits,
                                   save_operands)
+
+
+class ShortConvFunction(torch.autograd.Function):
+    """y, final_state = short_conv(x, weight, bias, h0) with gradients for all four."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, h0, cu_seqlens, cu_seqlens_dev, activation, output_final_state):
+        f = layers.short_conv(x, weight, bias=bias, h0=h0, cu_seqlens=cu_seqlens, cu_seqlens_dev=cu_seqlens_dev,
+                              activation=activation, output_final_state=output_final_state)
+        ctx.save_for_backward(x, weight, bias, h0, cu_seqlens_dev)
+        ctx.cu_seqlens, ctx.activation = cu_seqlens, activation
+        ctx.set_materialize_grads(False)
+        return f["y"], f["final_state"]
+
+    @staticmethod
+    def backward(ctx, dy, dfinal):
+        x, weight, bias, h0, cu_dev = ctx.saved_tensors
+        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
+        r = layers.short_conv_bwd(x, weight, dy, bias=bias, h0=h0, dfinal=None if dfinal is None else dfinal.contiguous(),
+                                  cu_seqlens=ctx.cu_seqlens, cu_seqlens_dev=cu_dev, activation=ctx.activation)
+        return r["dx"], r["dweight"], r["dbias"], r["dh0"], None, None, None, None
+
+
+def short_conv(x, weight, bias=None, h0=None, cu_seqlens=None, cu_seqlens_dev=None, activation="silu",
+               output_final_state=False):
+    """Differentiable ``layers.short_conv``. Returns (y, final_state or None)."""
+    return ShortConvFunction.apply(x, weight, bias, h0, cu_seqlens, cu_seqlens_dev, activation, output_final_state)
+
+
+class SelectiveScanFunction(torch.autograd.Function):
+    """y, final_state = selective_scan(x, dt, A, B, C, skip, z, dt_bias, h0) with gradients for all nine."""
+
+    @staticmethod
+    def forward(ctx, x, dt, A, B, C, skip, z, dt_bias, h0, cu_seqlens, cu_seqlens_dev, dt_softplus, output_final_state):
+        f = layers.selective_scan(x, dt, A, B, C, skip=skip, z=z, dt_bias=dt_bias, h0=h0, cu_seqlens=cu_seqlens,
+                                  cu_seqlens_dev=cu_seqlens_dev, dt_softplus=dt_softplus,
+                                  output_final_state=output_final_state, save=True)
+        ctx.save_for_backward(x, dt, A, B, C, skip, z, dt_bias, cu_seqlens_dev, f["states"])
+        ctx.cu_seqlens, ctx.dt_softplus, ctx.has_h0 = cu_seqlens, dt_softplus, h0 is not None
+        ctx.set_materialize_grads(False)
+        return f["y"], f["final_state"]
+
+    @staticmethod
+    def backward(ctx, dy, dfinal):
+        x, dt, A, B, C, skip, z, dt_bias, cu_dev, states = ctx.saved_tensors
+        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
+        r = layers.selective_scan_bwd(x, dt, A, B, C, states, dy, skip=skip, z=z, dt_bias=dt_bias,
+                                      dfinal=None if dfinal is None else dfinal.contiguous(), cu_seqlens=ctx.cu_seqlens,
+                                      cu_seqlens_dev=cu_dev, dt_softplus=ctx.dt_softplus, output_dh0=ctx.has_h0)
+        return (r["dx"], r["ddt"], r["dA"], r["dB"], r["dC"], r["dskip"], r["dz"], r["ddt_bias"], r["dh0"], None, None,
+                None, None)
+
+
+def selective_scan(x, dt, A, B, C, skip=None, z=None, dt_bias=None, h0=None, cu_seqlens=None, cu_seqlens_dev=None,
+                   dt_softplus=False, output_final_state=True):
+    """Differentiable ``layers.selective_scan``. Returns (y, final_state or None)."""
+    return SelectiveScanFunction.apply(x, dt, A, B, C, skip, z, dt_bias, h0, cu_seqlens, cu_seqlens_dev, dt_softplus,
+                                       output_final_state)
+
+
+class GroupNormFunction(torch.autograd.Function):
+    """y = group_norm(x, weight, bias, gate) with gradients for all four. The statistics are formed again
+    in the backward, which reads x in any case."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, gate, groups, activation, center, eps):
+        ctx.save_for_backward(x, weight, bias, gate)
+        ctx.args = dict(activation=activation, center=center, eps=eps)
+        ctx.groups = groups
+        return layers.group_norm(x, groups, weight=weight, bias=bias, gate=gate, **ctx.args)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, bias, gate = ctx.saved_tensors
+        r = layers.group_norm_bwd(x, ctx.groups, dy.contiguous(), weight=weight, bias=bias, gate=gate, **ctx.args)
+        return r["dx"], r["dweight"], r["dbias"], r["dgate"], None, None, None, None
+
+
+def group_norm(x, groups, weight=None, bias=None, gate=None, activation=None, center=False, eps=1e-5):
+    """Differentiable ``layers.group_norm``."""
+    return GroupNormFunction.apply(x, weight, bias, gate, groups, activation, center, eps)

@@ -44,8 +44,9 @@ kda_status check_dtype(int dtype) {
   return KDA_OK;
 }
 
-kda_status check_aligned(const void* p, const char* name) {
-  if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return fail(KDA_EINVAL, "%s must be 16-byte aligned", name);
+// Rows of states that fill a lane's four are read and written 16 bytes at a time.
+kda_status check_aligned(const void* p, const char* name, int NS) {
+  if (NS == kda::scan_np(NS) && reinterpret_cast<uintptr_t>(p) % 16 != 0) return fail(KDA_EINVAL, "%s must be 16-byte aligned", name);
   return KDA_OK;
 }
 
@@ -362,10 +363,10 @@ KDA_EXPORT kda_status kda_sscan_fwd(const kda_sscan_dims* dims, const void* x, c
     REQUIRE(Cm, "C");
     REQUIRE(y, "y");
   }
-  TRY(check_aligned(A, "A"));
-  TRY(check_aligned(h0, "h0"));
-  TRY(check_aligned(final_state, "final_state"));
-  TRY(check_aligned(states, "states"));
+  TRY(check_aligned(A, "A", dims->NS));
+  TRY(check_aligned(h0, "h0", dims->NS));
+  TRY(check_aligned(final_state, "final_state", dims->NS));
+  TRY(check_aligned(states, "states", dims->NS));
   const ScanLayout l = scan_layout(dims, t, false);
   TRY(check_ws(workspace, ws_bytes, l.total));
   a.x = x;
@@ -412,10 +413,10 @@ KDA_EXPORT kda_status kda_sscan_bwd(const kda_sscan_dims* dims, const void* x, c
   }
   if (dz != nullptr) REQUIRE(z, "z (needed for dz)");
   if (dskip != nullptr) REQUIRE(skip, "skip (needed for dskip)");
-  TRY(check_aligned(A, "A"));
-  TRY(check_aligned(states, "states"));
-  TRY(check_aligned(dfinal, "dfinal"));
-  TRY(check_aligned(dh0, "dh0"));
+  TRY(check_aligned(A, "A", dims->NS));
+  TRY(check_aligned(states, "states", dims->NS));
+  TRY(check_aligned(dfinal, "dfinal", dims->NS));
+  TRY(check_aligned(dh0, "dh0", dims->NS));
   const ScanLayout l = scan_layout(dims, t, true);
   TRY(check_ws(workspace, ws_bytes, l.total));
   a.x = x;
@@ -461,8 +462,8 @@ KDA_EXPORT kda_status kda_sscan_step(const kda_sscan_dims* dims, const void* x, 
   REQUIRE(Cm, "C");
   REQUIRE(state, "state");
   REQUIRE(y, "y");
-  TRY(check_aligned(A, "A"));
-  TRY(check_aligned(state, "state"));
+  TRY(check_aligned(A, "A", dims->NS));
+  TRY(check_aligned(state, "state", dims->NS));
   kda::ScanStepArgs a{};
   a.B = dims->B;
   a.D = dims->D;

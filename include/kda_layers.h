@@ -78,7 +78,8 @@ kda_status kda_short_conv_step(const kda_conv_dims* dims, const void* x, const f
 /* ---------------------------------------------------------------------------------------------
  * Selective state space scan. With dt_t = raw_t + dt_bias (softplus of it where dims->softplus):
  *   h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t,   y_t = <C_t, h_t> + skip x_t,   y_t *= silu(z_t),
- * per channel d with NS states; B and C are shared by the D / G channels of a group.
+ * per channel d with NS states; B and C are shared by the D / G channels of a group. Where NS is 8,
+ * 16, 32 or 64, the fp32 arrays with a last dimension NS must be 16-byte aligned.
  */
 #define KDA_SCAN_CHUNK 16 /* tokens between two saved states */
 
