@@ -33,6 +33,7 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 // grids (one dimension of workgroups) and the 32-bit token numbers of cu_seqlens.
 constexpr int64_t kMaxTokens = INT32_MAX - 64;
 constexpr int kMaxChannels = 1 << 20;
+constexpr int64_t kMaxRow = 1 << 25;
 constexpr int kMaxStepRows = 65535;  // second grid dimension
 
 kda_status hip_status(hipError_t e, const char* what) {
@@ -62,6 +63,8 @@ kda_status check_ws(void* ws, size_t ws_bytes, size_t need) {
 kda_status row_of(int64_t given, int64_t width, const char* name, int64_t* row) {
   if (given != 0 && given < width)
     return fail(KDA_EINVAL, "%s_row (%lld) must be 0 or at least the width (%lld)", name, (long long)given, (long long)width);
+  // the scan holds a chunk's offsets (16 rows) in 32 bits
+  if (given > kMaxRow) return fail(KDA_EINVAL, "%s_row must be at most %lld, got %lld", name, (long long)kMaxRow, (long long)given);
   *row = given == 0 ? width : given;
   return KDA_OK;
 }
@@ -254,38 +257,40 @@ kda_status sscan_check(const kda_sscan_dims* d, bool launching, Tokens* t, kda::
   a->G = d->G;
   a->softplus = d->softplus;
   const int64_t cols = (int64_t)d->G * kda::scan_tiles(d->D, d->NS, d->G);
-  // a segment has at least 64 tokens, or is a sequence of its own
-  if ((t->sq.total / 64 + d->N) * cols > INT32_MAX)
+  // a local segment has at least 16 tokens, or is a sequence of its own
+  if ((t->sq.total / 16 + d->N) * cols > INT32_MAX)
     return fail(KDA_EINVAL, "too many channel tiles (%lld tokens x %lld)", (long long)t->sq.total, (long long)cols);
   if (t->sq.total * d->G * d->NS / 256 > INT32_MAX) return fail(KDA_EINVAL, "too many tokens for G * NS = %d", d->G * d->NS);
   return KDA_OK;
 }
 
 struct ScanLayout {
-  int seg = 0;
-  int64_t nseg = 0, chunks = 0;
+  int seg = 0, lseg = 0;
+  int64_t nseg = 0, nloc = 0, chunks = 0;
   bool split = false;
-  size_t segoff = 0, choff = 0, seg_dt = 0, seg_state = 0, part_bc = 0, part_a = 0, part_d = 0, total = 0;
+  size_t segoff = 0, loff = 0, choff = 0, seg_dt = 0, seg_state = 0, part_bc = 0, part_a = 0, part_d = 0, total = 0;
 };
 
 ScanLayout scan_layout(const kda_sscan_dims* d, const Tokens& t, bool bwd) {
   ScanLayout l;
-  l.seg = kda::scan_seg(t.sq, t.longest, d->D, d->NS, d->G, bwd);
+  kda::scan_seg(t.sq, t.longest, d->D, d->NS, d->G, bwd, &l.seg, &l.lseg);
   l.split = t.longest > l.seg;
   for (int n = 0; n < d->N; ++n) {
     const int64_t len = d->cu_seqlens_host != nullptr ? d->cu_seqlens_host[n + 1] - d->cu_seqlens_host[n] : d->T;
     l.nseg += len > 0 ? (len + l.seg - 1) / l.seg : 1;
+    l.nloc += len > 0 ? (len + l.lseg - 1) / l.lseg : 1;
     l.chunks += (len + kda::kScanChunk - 1) / kda::kScanChunk;
   }
   const size_t NP = kda::scan_np(d->NS), D = d->D;
   size_t o = 0;
   if (d->cu_seqlens_host != nullptr) {
     l.segoff = o; o = align_up(o + sizeof(int32_t) * (d->N + 1));
+    l.loff = o; o = align_up(o + sizeof(int32_t) * (d->N + 1));
     l.choff = o; o = align_up(o + sizeof(int32_t) * (d->N + 1));
   }
   if (l.split) {
-    l.seg_dt = o; o = align_up(o + (size_t)l.nseg * D * sizeof(float));
-    l.seg_state = o; o = align_up(o + (size_t)l.nseg * D * NP * sizeof(float));
+    l.seg_dt = o; o = align_up(o + (size_t)l.nloc * D * sizeof(float));
+    l.seg_state = o; o = align_up(o + (size_t)l.nloc * D * NP * sizeof(float));
   }
   if (bwd) {
     l.part_bc = o; o = align_up(o + (size_t)kda::scan_tiles(d->D, d->NS, d->G) * t.sq.total * d->G * 2 * NP * sizeof(float));
@@ -301,6 +306,9 @@ void scan_use(const ScanLayout& l, void* workspace, kda::ScanArgs* a) {
   a->seg = l.seg;
   a->nseg = l.nseg;
   a->split = l.split;
+  a->lseg = l.lseg;
+  a->nloc = l.nloc;
+  a->loff = reinterpret_cast<int32_t*>(ws + l.loff);
   a->segoff = reinterpret_cast<int32_t*>(ws + l.segoff);
   a->choff = reinterpret_cast<int32_t*>(ws + l.choff);
   a->seg_dt = reinterpret_cast<float*>(ws + l.seg_dt);
@@ -321,7 +329,8 @@ int scan_vec(const kda::ScanArgs& a, int dtype, const void* const* ptrs, int np)
 kda_status scan_tables(const kda_sscan_dims* d, const ScanLayout& l, void* workspace, const kda::ScanArgs& a, hipStream_t st) {
   if (d->cu_seqlens_host == nullptr) return KDA_OK;
   char* ws = static_cast<char*>(workspace);
-  return hip_status(kda::launch_scan_tables(a.sq, l.seg, reinterpret_cast<int32_t*>(ws + l.segoff),
+  return hip_status(kda::launch_scan_tables(a.sq, l.seg, l.lseg, reinterpret_cast<int32_t*>(ws + l.segoff),
+                                            reinterpret_cast<int32_t*>(ws + l.loff),
                                             reinterpret_cast<int32_t*>(ws + l.choff), st), "segment table");
 }
 

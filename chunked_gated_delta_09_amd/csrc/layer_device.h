@@ -54,10 +54,13 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + exp2_hw(-kLog2e * x)); }
 // log(1 + e^x) = max(x, 0) + log1p(e^-|x|): no overflow, and full relative precision for very
 // negative x, where it is e^x. log1p(e) with u = 1 + e rounded is log(u) + (e - (u - 1)) / u.
-__device__ __forceinline__ float softplus(float x) {
+// `slope`: its derivative, 1 / (1 + e^-x).
+__device__ __forceinline__ float softplus(float x, float* slope = nullptr) {
   const float e = exp2_hw(-kLog2e * fabsf(x));
-  const float u = 1.f + e;
-  return fmaxf(x, 0.f) + (__logf(u) + (e - (u - 1.f)) * __builtin_amdgcn_rcpf(u));
+  const float u = 1.f + e, v = __builtin_amdgcn_rcpf(u);
+  if (slope != nullptr) *slope = x >= 0.f ? v : e * v;
+  // the median with 0 and infinity is max(x, 0) in one instruction
+  return __builtin_amdgcn_fmed3f(x, 0.f, __builtin_inff()) + (__logf(u) + (e - (u - 1.f)) * v);
 }
 
 // y = act(x) and its derivative for kda_act codes.
@@ -72,24 +75,33 @@ __device__ __forceinline__ float dact_f(float x, int act) {
   return act == KDA_ACT_SIGMOID ? s * (1.f - s) : s * (1.f + x * (1.f - s));
 }
 
-// Value of the lane whose number differs by the power of two D.
-template <int D>
-__device__ __forceinline__ float xor_lane(float x) {
+// Moves within rows of 16 lanes (DPP controls): quad permutations, mirrors, rotations, shifts.
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kRor8 = 0x128, kShl4 = 0x104;
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
   const int v = __float_as_int(x);
-  if constexpr (D == 1) return __int_as_float(__builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true));  // quad_perm 1,0,3,2
-  if constexpr (D == 2) return __int_as_float(__builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true));  // quad_perm 2,3,0,1
-  if constexpr (D > 2) return __shfl_xor(x, D, 64);
+  return __int_as_float(__builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, true));
+}
+// x + the value of the lane that differs in bit 4 (bit 5).
+__device__ __forceinline__ float add_xor16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float add_xor32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Sum over the L lanes of an aligned group (L a power of two).
+// Sum over the L lanes of an aligned group (L a power of two), in every lane. The mirror of 8 lanes
+// stands for the lane 4 away: the four lanes of a quad hold the same sum by then.
 template <int L>
 __device__ __forceinline__ float group_sum(float x) {
-  if constexpr (L >= 2) x += xor_lane<1>(x);
-  if constexpr (L >= 4) x += xor_lane<2>(x);
-  if constexpr (L >= 8) x += xor_lane<4>(x);
-  if constexpr (L >= 16) x += xor_lane<8>(x);
-  if constexpr (L >= 32) x += xor_lane<16>(x);
-  if constexpr (L >= 64) x += xor_lane<32>(x);
+  if constexpr (L >= 2) x += dpp<kXor1>(x);
+  if constexpr (L >= 4) x += dpp<kXor2>(x);
+  if constexpr (L >= 8) x += dpp<kHalfMirror>(x);
+  if constexpr (L >= 16) x += dpp<kRor8>(x);
+  if constexpr (L >= 32) x = add_xor16(x);
+  if constexpr (L >= 64) x = add_xor32(x);
   return x;
 }
 

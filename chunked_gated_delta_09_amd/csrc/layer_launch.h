@@ -65,8 +65,11 @@ struct ScanArgs {
   const int32_t* segoff;    // packed: [n + 1] first segment of each sequence
   const int32_t* choff;     // packed: [n + 1] first chunk of each sequence
   int split;                // some sequence has more than one segment
-  float* seg_dt;            // [nseg][D] sum of dt over the segment
-  float* seg_state;         // [nseg][D][NP] what the segment adds to the carried state
+  int lseg;                 // tokens of a local segment (divides seg)
+  int64_t nloc;             // local segments in all
+  const int32_t* loff;      // packed: [n + 1] first local segment of each sequence
+  float* seg_dt;            // [nloc][D] sum of dt over the local segment
+  float* seg_state;         // [nloc][D][NP] what the local segment adds to the carried state
   float* part_bc;           // bwd [tiles of a group][tokens][G][2 NP]
   float* part_a;            // bwd [nseg][D][NP]
   float* part_d;            // bwd [nseg][2][D]: dskip, ddt_bias
@@ -74,8 +77,9 @@ struct ScanArgs {
 };
 int scan_np(int N);                      // padded states
 int scan_tiles(int D, int N, int G);     // channel tiles of one group
-int scan_seg(const Seqs& s, int64_t longest, int D, int N, int G, bool bwd);
-hipError_t launch_scan_tables(const Seqs& s, int seg, int32_t* segoff, int32_t* choff, hipStream_t st);
+void scan_seg(const Seqs& s, int64_t longest, int D, int N, int G, bool bwd, int* seg, int* lseg);
+hipError_t launch_scan_tables(const Seqs& s, int seg, int lseg, int32_t* segoff, int32_t* loff, int32_t* choff,
+                              hipStream_t st);
 hipError_t launch_sscan_fwd(int dtype, const ScanArgs& a, hipStream_t st);
 hipError_t launch_sscan_bwd(int dtype, const ScanArgs& a, hipStream_t st);
 

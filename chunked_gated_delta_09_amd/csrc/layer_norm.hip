@@ -12,12 +12,12 @@ namespace {
 // Sum over the tpi lanes of a group. tpi = 256: the whole workgroup, through `sh` (4 floats; two
 // buffers alternate, so one barrier a sum is enough).
 __device__ __forceinline__ float item_sum(float x, int tpi, float* sh) {
-  if (tpi >= 2) x += xor_lane<1>(x);
-  if (tpi >= 4) x += xor_lane<2>(x);
-  if (tpi >= 8) x += xor_lane<4>(x);
-  if (tpi >= 16) x += xor_lane<8>(x);
-  if (tpi >= 32) x += xor_lane<16>(x);
-  if (tpi >= 64) x += xor_lane<32>(x);
+  if (tpi >= 2) x += dpp<kXor1>(x);
+  if (tpi >= 4) x += dpp<kXor2>(x);
+  if (tpi >= 8) x += dpp<kHalfMirror>(x);
+  if (tpi >= 16) x += dpp<kRor8>(x);
+  if (tpi >= 32) x = add_xor16(x);
+  if (tpi >= 64) x = add_xor32(x);
   if (tpi == 256) {
     if (threadIdx.x % 64 == 0) sh[threadIdx.x / 64] = x;
     __syncthreads();

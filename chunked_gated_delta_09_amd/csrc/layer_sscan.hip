@@ -7,10 +7,11 @@
 // itself stays in registers. The work is bound by the vector unit, mostly by the one exponential a
 // state and token needs (a quarter-rate instruction).
 //
-// A call with few channels and sequences is cut along the tokens too: a first pass over all
-// segments but a sequence's last finds what each adds to the carried state, h_out = exp(A sum dt)
-// h_in + loc, and every segment of the second pass joins those before it on entry. That runs the
-// recurrence twice, so it is only done where the uncut grid leaves the chip idle (scan_seg).
+// A call with few channels and sequences is cut along the tokens too: a first pass finds what each
+// local segment adds to the carried state, h_out = exp(A sum dt) h_in + loc, and every segment of the
+// second pass joins those before it on entry. That runs the recurrence twice, so it is only done
+// where the uncut grid leaves the chip idle (scan_seg). Local segments may be shorter: the first
+// pass has fewer registers, and so room for more workgroups at a time.
 #include "layer_device.h"
 
 namespace kda {
@@ -20,35 +21,42 @@ namespace {
 constexpr int TT = kScanChunk;
 constexpr int NPL = kScanStates;
 
-// The segment of a workgroup.
+// A run of tokens of one sequence, as a workgroup takes it.
 struct Segment {
   int n;               // sequence
-  int j, count;        // place among the sequence's segments, their number
-  int64_t first;       // the sequence's first segment
+  int j, count;        // place among the sequence's segments of this length, their number
+  int64_t first;       // the first of them
   int64_t t0;          // first token
   int len;             // tokens
-  int64_t chunk0;      // first chunk
 };
 
-__device__ __forceinline__ Segment segment_at(const ScanArgs& a, int64_t s) {
+// Segments of `seg` tokens in a sequence of `len`.
+__device__ __forceinline__ int segments_of(int64_t len, int seg) { return len > 0 ? (int)((len + seg - 1) / seg) : 1; }
+
+// Segment s of length seg; off: the first segment of each packed sequence.
+__device__ __forceinline__ Segment segment_at(const Seqs& sq, int64_t s, int seg, const int32_t* off) {
   Segment g;
-  if (a.sq.cu != nullptr) {
-    g.n = find_seq(a.segoff, a.sq.n, s);
-    g.first = a.segoff[g.n];
-    g.count = (int)(a.segoff[g.n + 1] - g.first);
-    g.chunk0 = a.choff[g.n];
+  if (sq.cu != nullptr) {
+    g.n = find_seq(off, sq.n, s);
+    g.first = off[g.n];
+    g.count = (int)(off[g.n + 1] - g.first);
   } else {
-    g.count = a.sq.T > 0 ? (a.sq.T + a.seg - 1) / a.seg : 1;
+    g.count = segments_of(sq.T, seg);
     g.n = (int)(s / g.count);
     g.first = (int64_t)g.n * g.count;
-    g.chunk0 = (int64_t)g.n * ((a.sq.T + TT - 1) / TT);
   }
   g.j = (int)(s - g.first);
-  const int64_t begin = seq_begin(a.sq, g.n), end = seq_end(a.sq, g.n);
-  g.t0 = begin + (int64_t)g.j * a.seg;
-  g.len = (int)min((int64_t)a.seg, end - g.t0);
-  g.chunk0 += (int64_t)g.j * (a.seg / TT);
+  g.t0 = seq_begin(sq, g.n) + (int64_t)g.j * seg;
+  g.len = (int)min((int64_t)seg, seq_end(sq, g.n) - g.t0);
   return g;
+}
+__device__ __forceinline__ int64_t first_chunk(const ScanArgs& a, const Segment& g) {
+  const int64_t first = a.sq.cu != nullptr ? a.choff[g.n] : (int64_t)g.n * ((a.sq.T + TT - 1) / TT);
+  return first + (int64_t)g.j * (a.seg / TT);
+}
+// A sequence's local segments (lseg tokens each).
+__device__ __forceinline__ int64_t first_local(const ScanArgs& a, int n) {
+  return a.sq.cu != nullptr ? a.loff[n] : (int64_t)n * segments_of(a.sq.T, a.lseg);
 }
 
 // What a workgroup's lanes are.
@@ -90,6 +98,109 @@ __device__ __forceinline__ void store_states(float* p, int64_t row, int N, int p
     if (part * NPL + i < N) p[row * N + part * NPL + i] = v[i];
 }
 
+// Carries h through `count` segments from `s` on (step: the one behind or before): h <- exp(A sum dt) h +
+// loc. Eight segments are loaded together, since only the sums depend on each other.
+template <int NP>
+__device__ __forceinline__ void join_segments(const ScanArgs& a, int64_t s, int step, int64_t count, int64_t d, int part,
+                                              const float (&A2)[NPL], float (&h)[NPL]) {
+  for (int64_t k = 0; k < count; k += 8) {
+    float sum[8];
+    float4 loc[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (k + u < count) {
+        const int64_t row = (s + (int64_t)step * (k + u)) * a.D + d;
+        sum[u] = a.seg_dt[row];
+        loc[u] = *reinterpret_cast<const float4*>(a.seg_state + row * NP + part * NPL);
+      }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (k + u < count) {
+        const float add[NPL] = {loc[u].x, loc[u].y, loc[u].z, loc[u].w};
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) h[i] = fmaf(exp2_hw(sum[u] * A2[i]), h[i], add[i]);
+      }
+  }
+}
+
+// What a thread stages of a chunk: four neighbouring channels of one token (ITEMS such pieces) and
+// BCI elements of B and C. Addresses are a chunk's base, the same for the workgroup, and 32-bit byte
+// offsets that stay the same for all chunks.
+template <class T, int NP>
+struct Stage {
+  typedef Lanes<NP> L;
+  int tid, per, grp, c0;
+  bool inner;  // all channels of the tile exist, four-element loads are aligned
+
+  __device__ __forceinline__ Stage(const ScanArgs& a, int grp_, int c0_)
+      : tid(threadIdx.x), per(a.D / a.G), grp(grp_), c0(c0_), inner(a.vec != 0 && c0_ + L::CH <= a.D / a.G) {}
+  // To be called once a chunk: what follows from the thread's number (places, masks, the addresses of
+  // partial chunks) is formed again rather than kept in registers across the recurrence.
+  __device__ __forceinline__ void renew() { asm volatile("" : "+v"(tid)); }
+  __device__ __forceinline__ bool has(int k) const { return TT * L::Q >= 256 * (k + 1) || tid + k * 256 < TT * L::Q; }
+  __device__ __forceinline__ int token(int k) const { return (tid + k * 256) / L::Q; }
+  __device__ __forceinline__ int col(int k) const { return (tid + k * 256) % L::Q * 4; }
+  __device__ __forceinline__ int bc_token(int k) const { return (tid + k * 256) / NP; }
+  __device__ __forceinline__ int bc_state(int k) const { return (tid + k * 256) % NP; }
+  __device__ __forceinline__ bool bc_has(int k) const { return TT * NP >= 256 * (k + 1) || tid + k * 256 < TT * NP; }
+  // this thread's place from the chunk's first row on
+  __device__ __forceinline__ uint32_t offset(int k, int64_t row) const {
+    return (uint32_t)((token(k) * row + (int64_t)grp * per + c0 + col(k)) * (int64_t)sizeof(T));
+  }
+  __device__ __forceinline__ uint32_t bc_offset(int k, int64_t row, int N) const {
+    return (uint32_t)((bc_token(k) * row + (int64_t)grp * N + bc_state(k)) * (int64_t)sizeof(T));
+  }
+  // piece k of the chunk whose first token is t and that has `live` tokens
+  __device__ __forceinline__ Vec<T, 4> load(const void* p, int64_t t, int64_t row, uint32_t off, int k, int live) const {
+    const T* q = reinterpret_cast<const T*>(static_cast<const char*>(p) + t * row * (int64_t)sizeof(T) + off);
+    if (inner && live >= TT) {
+      if (has(k)) return *reinterpret_cast<const Vec<T, 4>*>(q);
+      return Vec<T, 4>{};
+    }
+    return load_n<T, 4>(q, has(k) && token(k) < live ? per - c0 - col(k) : 0, inner);
+  }
+  __device__ __forceinline__ T load_bc(const void* p, int64_t t, int64_t row, uint32_t off, int k, int N, int live) const {
+    const T* q = reinterpret_cast<const T*>(static_cast<const char*>(p) + t * row * (int64_t)sizeof(T) + off);
+    return bc_has(k) && bc_token(k) < live && bc_state(k) < N ? *q : (T)0.f;
+  }
+  __device__ __forceinline__ void store(void* p, int64_t t, int64_t row, uint32_t off, int k, int live,
+                                        const float (&v)[4]) const {
+    T* q = reinterpret_cast<T*>(static_cast<char*>(p) + t * row * (int64_t)sizeof(T) + off);
+    if (has(k) && token(k) < live) store_n<T, 4>(q, v, inner ? 4 : per - c0 - col(k), inner);
+  }
+  // a parameter of the tile's channels to shared memory
+  __device__ __forceinline__ void params(const float* p, float* to) const {
+    if (tid < L::CH) to[tid] = p != nullptr && c0 + tid < per ? p[(int64_t)grp * per + c0 + tid] : 0.f;
+  }
+};
+
+__device__ __forceinline__ void unpack(const float4& v, float (&out)[4]) {
+  out[0] = v.x;
+  out[1] = v.y;
+  out[2] = v.z;
+  out[3] = v.w;
+}
+
+// The staging threads' sums of dt (16 a channel) to seg_dt of segment s; sh: [TT][CH].
+template <class T, int NP>
+__device__ __forceinline__ void sum_dt(const ScanArgs& a, const Stage<T, NP>& sv, const float (&total)[Lanes<NP>::ITEMS][4],
+                                       float* sh, int64_t s) {
+  typedef Lanes<NP> L;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < L::ITEMS; ++k)
+    if (sv.has(k))
+      *reinterpret_cast<float4*>(sh + sv.token(k) * L::CH + sv.col(k)) =
+          make_float4(total[k][0], total[k][1], total[k][2], total[k][3]);
+  __syncthreads();
+  if (sv.tid < L::CH && sv.c0 + sv.tid < sv.per) {
+    float sum = 0.f;
+#pragma unroll
+    for (int t = 0; t < TT; ++t) sum += sh[t * L::CH + sv.tid];
+    a.seg_dt[s * a.D + (int64_t)sv.grp * sv.per + sv.c0 + sv.tid] = sum;
+  }
+}
+
 // Forward. OUT: y, saved and final states; otherwise only what the segment adds to the state.
 template <class T, int NP, bool OUT>
 __global__ __launch_bounds__(256) void sscan_fwd_kernel(ScanArgs a, int tiles) {
@@ -97,15 +208,16 @@ __global__ __launch_bounds__(256) void sscan_fwd_kernel(ScanArgs a, int tiles) {
   __shared__ float2 sX[TT][L::CH];          // dt, dt x
   __shared__ float sB[TT][NP], sC[OUT ? TT : 1][NP];
   __shared__ float sY[OUT ? TT : 1][L::CH];
-  const int per = a.D / a.G;                // channels of a group
+  __shared__ float sBias[L::CH], sSkip[L::CH];
   const int bx = blockIdx.x % (a.G * tiles), grp = bx / tiles;
   const int c0 = (bx % tiles) * L::CH;      // first channel, within the group
-  const Segment sg = segment_at(a, blockIdx.x / (a.G * tiles));
-  if (!OUT && sg.j == sg.count - 1) return;
+  const Segment sg = segment_at(a.sq, blockIdx.x / (a.G * tiles), OUT ? a.seg : a.lseg, OUT ? a.segoff : a.loff);
+  // the last segment of the second pass has no successor to carry its state to
+  if (!OUT && sg.j >= (segments_of(seq_end(a.sq, sg.n) - seq_begin(a.sq, sg.n), a.seg) - 1) * (a.seg / a.lseg)) return;
+  Stage<T, NP> sv(a, grp, c0);
   const int tid = threadIdx.x, part = tid % L::LPC, chl = tid / L::LPC;
-  const bool in = c0 + chl < per;
-  const int64_t d = (int64_t)grp * per + c0 + chl;
-  const bool vec = a.vec != 0;
+  const bool in = c0 + chl < sv.per;
+  const int64_t d = (int64_t)grp * sv.per + c0 + chl;
 
   float A2[NPL], h[NPL];  // exp(dt A) = 2^(dt A log2 e): the factor is folded into A once
   load_states<NP>(a.A, d, a.N, part, in, A2);
@@ -116,126 +228,122 @@ __global__ __launch_bounds__(256) void sscan_fwd_kernel(ScanArgs a, int tiles) {
   }
   if (OUT) {
     if (a.h0 != nullptr) load_states<NP>(a.h0, (int64_t)sg.n * a.D + d, a.N, part, in, h);
-    if (in)
-      for (int64_t s = sg.first; s < sg.first + sg.j; ++s) {
-        const float sum = a.seg_dt[s * a.D + d];
-        const float4 loc = *reinterpret_cast<const float4*>(a.seg_state + (s * a.D + d) * NP + part * NPL);
-        const float add[NPL] = {loc.x, loc.y, loc.z, loc.w};
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) h[i] = fmaf(exp2_hw(sum * A2[i]), h[i], add[i]);
-      }
+    if (in && a.split)
+      join_segments<NP>(a, first_local(a, sg.n), 1, (int64_t)sg.j * (a.seg / a.lseg), d, part, A2, h);
   }
-  float total = 0.f;  // sum of dt
+  const int64_t chunk0 = OUT ? first_chunk(a, sg) : 0;
+  float total[L::ITEMS][4] = {};  // sum of dt over the tokens that this thread stages
+  sv.params(a.dt_bias, sBias);
+  if (OUT) sv.params(a.skip, sSkip);
 
-  // staged pieces: token pt of the chunk, channels pc .. pc + 3
-  float bias[L::ITEMS][4], skip[L::ITEMS][4];
   Vec<T, 4> rx[L::ITEMS], rd[L::ITEMS], rz[L::ITEMS];
   T rb[L::BCI], rc[L::BCI];
+  uint32_t ox[L::ITEMS], od[L::ITEMS], oz[L::ITEMS], oy[L::ITEMS], ob[L::BCI], oc[L::BCI];
 #pragma unroll
   for (int k = 0; k < L::ITEMS; ++k) {
-    const int pc = c0 + (tid + k * 256) % L::Q * 4;
+    ox[k] = sv.offset(k, a.x_row);
+    od[k] = sv.offset(k, a.dt_row);
+    oz[k] = sv.offset(k, a.z_row);
+    oy[k] = sv.offset(k, a.D);
+  }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const bool ok = tid + k * 256 < TT * L::Q && pc + e < per;
-      bias[k][e] = ok && a.dt_bias != nullptr ? a.dt_bias[(int64_t)grp * per + pc + e] : 0.f;
-      skip[k][e] = OUT && ok && a.skip != nullptr ? a.skip[(int64_t)grp * per + pc + e] : 0.f;
-    }
+  for (int k = 0; k < L::BCI; ++k) {
+    ob[k] = sv.bc_offset(k, a.b_row, a.N);
+    oc[k] = sv.bc_offset(k, a.c_row, a.N);
   }
   auto fetch = [&](int at) {  // the chunk that begins at token `at` of the segment
+    const int64_t t = sg.t0 + at;
+    const int live = sg.len - at;
 #pragma unroll
     for (int k = 0; k < L::ITEMS; ++k) {
-      const int p = tid + k * 256, pt = at + p / L::Q, pc = c0 + p % L::Q * 4;
-      const int valid = p < TT * L::Q && pt < sg.len ? per - pc : 0;
-      const int64_t t = sg.t0 + pt, col = (int64_t)grp * per + pc;
-      rx[k] = load_n<T, 4>(static_cast<const T*>(a.x) + t * a.x_row + col, valid, vec);
-      rd[k] = load_n<T, 4>(static_cast<const T*>(a.dt) + t * a.dt_row + col, valid, vec);
-      if (OUT && a.z != nullptr) rz[k] = load_n<T, 4>(static_cast<const T*>(a.z) + t * a.z_row + col, valid, vec);
+      rx[k] = sv.load(a.x, t, a.x_row, ox[k], k, live);
+      rd[k] = sv.load(a.dt, t, a.dt_row, od[k], k, live);
+      if (OUT && a.z != nullptr) rz[k] = sv.load(a.z, t, a.z_row, oz[k], k, live);
     }
 #pragma unroll
     for (int k = 0; k < L::BCI; ++k) {
-      const int p = tid + k * 256, pt = at + p / NP, n = p % NP;
-      const bool ok = p < TT * NP && pt < sg.len && n < a.N;
-      const int64_t t = sg.t0 + pt;
-      rb[k] = ok ? static_cast<const T*>(a.B)[t * a.b_row + (int64_t)grp * a.N + n] : (T)0.f;
-      if (OUT) rc[k] = ok ? static_cast<const T*>(a.C)[t * a.c_row + (int64_t)grp * a.N + n] : (T)0.f;
+      rb[k] = sv.load_bc(a.B, t, a.b_row, ob[k], k, a.N, live);
+      if (OUT) rc[k] = sv.load_bc(a.C, t, a.c_row, oc[k], k, a.N, live);
     }
   };
   if (sg.len > 0) fetch(0);
+  __syncthreads();
   for (int at = 0; at < sg.len; at += TT) {
+    sv.renew();
+    const int live = sg.len - at;
     Vec<T, 4> kx[L::ITEMS], kz[L::ITEMS];  // this chunk's, for its outputs
 #pragma unroll
     for (int k = 0; k < L::ITEMS; ++k) {
-      const int p = tid + k * 256, pt = p / L::Q;
       kx[k] = rx[k];
       kz[k] = rz[k];
-      if (p < TT * L::Q) {
+      if (sv.has(k)) {
         // a token behind the segment's end gets dt = 0: it leaves the state as it is
-        const bool live = at + pt < sg.len;
+        const bool ok = sv.token(k) < live;
+        float bias[4];
+        unpack(*reinterpret_cast<const float4*>(&sBias[sv.col(k)]), bias);
+        float2* to = &sX[sv.token(k)][sv.col(k)];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float dt = as_f(rd[k].v[e]) + bias[k][e];
+          float dt = as_f(rd[k].v[e]) + bias[e];
           if (a.softplus) dt = softplus(dt);
-          dt = live ? dt : 0.f;
-          sX[pt][p % L::Q * 4 + e] = make_float2(dt, dt * as_f(rx[k].v[e]));
+          dt = ok ? dt : 0.f;
+          if (!OUT) total[k][e] += dt;
+          to[e] = make_float2(dt, dt * as_f(rx[k].v[e]));
         }
       }
     }
 #pragma unroll
-    for (int k = 0; k < L::BCI; ++k) {
-      const int p = tid + k * 256;
-      if (p < TT * NP) {
-        sB[p / NP][p % NP] = as_f(rb[k]);
-        if (OUT) sC[p / NP][p % NP] = as_f(rc[k]);
+    for (int k = 0; k < L::BCI; ++k)
+      if (sv.bc_has(k)) {
+        sB[sv.bc_token(k)][sv.bc_state(k)] = as_f(rb[k]);
+        if (OUT) sC[sv.bc_token(k)][sv.bc_state(k)] = as_f(rc[k]);
       }
-    }
     __syncthreads();
-    if (at + TT < sg.len) fetch(at + TT);
-    if (OUT && a.states != nullptr) store_states<NP>(a.states, (sg.chunk0 + at / TT) * a.D + d, a.N, part, in, h);
+    if (live > TT) fetch(at + TT);
+    if (OUT && a.states != nullptr) store_states<NP>(a.states, (chunk0 + at / TT) * a.D + d, a.N, part, in, h);
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
       const float2 v = sX[t][chl];
-      const float4 b4 = *reinterpret_cast<const float4*>(&sB[t][part * NPL]);
-      const float bb[NPL] = {b4.x, b4.y, b4.z, b4.w};
-      float y = 0.f;
-      if (!OUT) total += v.x;
+      float bb[NPL];
+      unpack(*reinterpret_cast<const float4*>(&sB[t][part * NPL]), bb);
 #pragma unroll
       for (int i = 0; i < NPL; ++i) h[i] = fmaf(exp2_hw(v.x * A2[i]), h[i], v.y * bb[i]);
       if (OUT) {
-        const float4 c4 = *reinterpret_cast<const float4*>(&sC[t][part * NPL]);
-        const float cc[NPL] = {c4.x, c4.y, c4.z, c4.w};
+        float cc[NPL];
+        unpack(*reinterpret_cast<const float4*>(&sC[t][part * NPL]), cc);
+        float y = cc[0] * h[0];
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) y = fmaf(cc[i], h[i], y);
-        y = group_sum<L::LPC>(y);
-        if (part == 0) sY[t][chl] = y;
+        for (int i = 1; i < NPL; ++i) y = fmaf(cc[i], h[i], y);
+        sY[t][chl] = group_sum<L::LPC>(y);  // the same from all lanes of the channel
       }
     }
     __syncthreads();
     if (OUT) {
 #pragma unroll
-      for (int k = 0; k < L::ITEMS; ++k) {
-        const int p = tid + k * 256, pt = p / L::Q, pc = p % L::Q * 4;
-        if (p < TT * L::Q && at + pt < sg.len) {
-          float out[4];
+      for (int k = 0; k < L::ITEMS; ++k)
+        if (sv.has(k)) {
+          float skip[4], out[4];
+          unpack(*reinterpret_cast<const float4*>(&sSkip[sv.col(k)]), skip);
+          unpack(*reinterpret_cast<const float4*>(&sY[sv.token(k)][sv.col(k)]), out);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            out[e] = fmaf(skip[k][e], as_f(kx[k].v[e]), sY[pt][pc + e]);
+            out[e] = fmaf(skip[e], as_f(kx[k].v[e]), out[e]);
             if (a.z != nullptr) {
               const float z = as_f(kz[k].v[e]);
               out[e] *= z * sigmoid(z);
             }
           }
-          store_n<T, 4>(static_cast<T*>(a.y) + (sg.t0 + at + pt) * a.D + (int64_t)grp * per + c0 + pc, out, per - c0 - pc, vec);
+          sv.store(a.y, sg.t0 + at, a.D, oy[k], k, live, out);
         }
-      }
     }
   }
   if (OUT) {
     if (a.final_state != nullptr && sg.j == sg.count - 1)
       store_states<NP>(a.final_state, (int64_t)sg.n * a.D + d, a.N, part, in, h);
-  } else if (in) {
+  } else {
     const int64_t s = sg.first + sg.j;
-    if (part == 0) a.seg_dt[s * a.D + d] = total;
-    *reinterpret_cast<float4*>(a.seg_state + (s * a.D + d) * NP + part * NPL) = make_float4(h[0], h[1], h[2], h[3]);
+    if (in) *reinterpret_cast<float4*>(a.seg_state + (s * a.D + d) * NP + part * NPL) = make_float4(h[0], h[1], h[2], h[3]);
+    sum_dt<T, NP>(a, sv, total, reinterpret_cast<float*>(sX), s);
   }
 }
 
@@ -247,15 +355,15 @@ __global__ __launch_bounds__(256) void sscan_bwd_local_kernel(ScanArgs a, int ti
   typedef Lanes<NP> L;
   __shared__ float2 sX[TT][L::CH];          // dt, dy'
   __shared__ float sC[TT][NP];
-  const int per = a.D / a.G;
+  __shared__ float sBias[L::CH];
   const int bx = blockIdx.x % (a.G * tiles), grp = bx / tiles;
   const int c0 = (bx % tiles) * L::CH;
-  const Segment sg = segment_at(a, blockIdx.x / (a.G * tiles));
-  if (sg.j == 0) return;
+  const Segment sg = segment_at(a.sq, blockIdx.x / (a.G * tiles), a.lseg, a.loff);
+  if (sg.j < a.seg / a.lseg) return;  // the first segment of the second pass has no predecessor
+  Stage<T, NP> sv(a, grp, c0);
   const int tid = threadIdx.x, part = tid % L::LPC, chl = tid / L::LPC;
-  const bool in = c0 + chl < per;
-  const int64_t d = (int64_t)grp * per + c0 + chl;
-  const bool vec = a.vec != 0;
+  const bool in = c0 + chl < sv.per;
+  const int64_t d = (int64_t)grp * sv.per + c0 + chl;
   float A2[NPL], q[NPL];
   load_states<NP>(a.A, d, a.N, part, in, A2);
 #pragma unroll
@@ -263,84 +371,80 @@ __global__ __launch_bounds__(256) void sscan_bwd_local_kernel(ScanArgs a, int ti
     A2[i] *= kLog2e;
     q[i] = 0.f;
   }
-  float total = 0.f;
-  float bias[L::ITEMS][4];
+  float total[L::ITEMS][4] = {};
+  sv.params(a.dt_bias, sBias);
   Vec<T, 4> rd[L::ITEMS], rz[L::ITEMS], ry[L::ITEMS];
   T rc[L::BCI];
+  uint32_t od[L::ITEMS], oz[L::ITEMS], oy[L::ITEMS], oc[L::BCI];
 #pragma unroll
   for (int k = 0; k < L::ITEMS; ++k) {
-    const int pc = c0 + (tid + k * 256) % L::Q * 4;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const bool ok = tid + k * 256 < TT * L::Q && pc + e < per;
-      bias[k][e] = ok && a.dt_bias != nullptr ? a.dt_bias[(int64_t)grp * per + pc + e] : 0.f;
-    }
+    od[k] = sv.offset(k, a.dt_row);
+    oz[k] = sv.offset(k, a.z_row);
+    oy[k] = sv.offset(k, a.D);
   }
+#pragma unroll
+  for (int k = 0; k < L::BCI; ++k) oc[k] = sv.bc_offset(k, a.c_row, a.N);
   auto fetch = [&](int at) {
+    const int64_t t = sg.t0 + at;
+    const int live = sg.len - at;
 #pragma unroll
     for (int k = 0; k < L::ITEMS; ++k) {
-      const int p = tid + k * 256, pt = at + p / L::Q, pc = c0 + p % L::Q * 4;
-      const int valid = p < TT * L::Q && pt < sg.len ? per - pc : 0;
-      const int64_t t = sg.t0 + pt, col = (int64_t)grp * per + pc;
-      rd[k] = load_n<T, 4>(static_cast<const T*>(a.dt) + t * a.dt_row + col, valid, vec);
-      ry[k] = load_n<T, 4>(static_cast<const T*>(a.dy) + t * a.D + col, valid, vec);
-      if (a.z != nullptr) rz[k] = load_n<T, 4>(static_cast<const T*>(a.z) + t * a.z_row + col, valid, vec);
+      rd[k] = sv.load(a.dt, t, a.dt_row, od[k], k, live);
+      ry[k] = sv.load(a.dy, t, a.D, oy[k], k, live);
+      if (a.z != nullptr) rz[k] = sv.load(a.z, t, a.z_row, oz[k], k, live);
     }
 #pragma unroll
-    for (int k = 0; k < L::BCI; ++k) {
-      const int p = tid + k * 256, pt = at + p / NP, n = p % NP;
-      const bool ok = p < TT * NP && pt < sg.len && n < a.N;
-      rc[k] = ok ? static_cast<const T*>(a.C)[(sg.t0 + pt) * a.c_row + (int64_t)grp * a.N + n] : (T)0.f;
-    }
+    for (int k = 0; k < L::BCI; ++k) rc[k] = sv.load_bc(a.C, t, a.c_row, oc[k], k, a.N, live);
   };
   const int last = (sg.len - 1) / TT * TT;
   if (sg.len > 0) fetch(last);
+  __syncthreads();
   for (int at = last; at >= 0 && sg.len > 0; at -= TT) {
+    sv.renew();
+    const int live = sg.len - at;
 #pragma unroll
-    for (int k = 0; k < L::ITEMS; ++k) {
-      const int p = tid + k * 256, pt = p / L::Q;
-      if (p < TT * L::Q) {
-        const bool live = at + pt < sg.len;
+    for (int k = 0; k < L::ITEMS; ++k)
+      if (sv.has(k)) {
+        const bool ok = sv.token(k) < live;
+        float bias[4];
+        unpack(*reinterpret_cast<const float4*>(&sBias[sv.col(k)]), bias);
+        float2* to = &sX[sv.token(k)][sv.col(k)];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float dt = as_f(rd[k].v[e]) + bias[k][e];
+          float dt = as_f(rd[k].v[e]) + bias[e];
           if (a.softplus) dt = softplus(dt);
+          dt = ok ? dt : 0.f;
+          total[k][e] += dt;
           float g = as_f(ry[k].v[e]);
           if (a.z != nullptr) {
             const float z = as_f(rz[k].v[e]);
             g *= z * sigmoid(z);
           }
-          sX[pt][p % L::Q * 4 + e] = make_float2(live ? dt : 0.f, live ? g : 0.f);
+          to[e] = make_float2(dt, g);
         }
       }
-    }
 #pragma unroll
-    for (int k = 0; k < L::BCI; ++k) {
-      const int p = tid + k * 256;
-      if (p < TT * NP) sC[p / NP][p % NP] = as_f(rc[k]);
-    }
+    for (int k = 0; k < L::BCI; ++k)
+      if (sv.bc_has(k)) sC[sv.bc_token(k)][sv.bc_state(k)] = as_f(rc[k]);
     __syncthreads();
     if (at > 0) fetch(at - TT);
 #pragma unroll
     for (int t = TT - 1; t >= 0; --t) {
       const float2 v = sX[t][chl];
-      const float4 c4 = *reinterpret_cast<const float4*>(&sC[t][part * NPL]);
-      const float cc[NPL] = {c4.x, c4.y, c4.z, c4.w};
-      total += v.x;
+      float cc[NPL];
+      unpack(*reinterpret_cast<const float4*>(&sC[t][part * NPL]), cc);
 #pragma unroll
       for (int i = 0; i < NPL; ++i) q[i] = exp2_hw(v.x * A2[i]) * fmaf(cc[i], v.y, q[i]);
     }
     __syncthreads();
   }
-  if (in) {
-    const int64_t s = sg.first + sg.j;
-    if (part == 0) a.seg_dt[s * a.D + d] = total;
-    *reinterpret_cast<float4*>(a.seg_state + (s * a.D + d) * NP + part * NPL) = make_float4(q[0], q[1], q[2], q[3]);
-  }
+  const int64_t s = sg.first + sg.j;
+  if (in) *reinterpret_cast<float4*>(a.seg_state + (s * a.D + d) * NP + part * NPL) = make_float4(q[0], q[1], q[2], q[3]);
+  sum_dt<T, NP>(a, sv, total, reinterpret_cast<float*>(sX), s);
 }
 
-// Pairs of values whose lanes differ in bit D: a lane keeps the first value's sum over the pair of
-// lanes where its bit is clear, the second's where it is set.
+// Joins two values over the lanes that differ in bit D: a lane keeps the first value's sum where
+// its bit is clear, the second's where it is set.
 template <int D>
 __device__ __forceinline__ float merge(float x, float y, int lane) {
   if constexpr (D == 32) {
@@ -351,243 +455,272 @@ __device__ __forceinline__ float merge(float x, float y, int lane) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
   }
-  if constexpr (D < 16) {
-    const bool up = lane & D;
+  if constexpr (D == 8) {
+    const bool up = lane & 8;
     const float keep = up ? y : x, give = up ? x : y;
-    return keep + xor_lane<D>(give);
+    return keep + dpp<kRor8>(give);
   }
 }
 
-// Backward of a segment, chunk by chunk from its end. From the saved state that enters a chunk the
-// 16 states and decays are formed again into registers; then, in reverse, with dy' = dy silu(z),
+// Backward of a segment, chunk by chunk from its end. From the saved state that enters a chunk its
+// states and decays are formed again, the later half of the chunk first, into registers; then, in
+// reverse, with dy' = dy silu(z),
 //   r = C dy' + q,   q <- a r,   p = q h_{t-1},
 //   dC += dy' h (summed over the group's channels),  dB += r dt x,  dA += dt p,
 //   dx = dt sum_n r B + skip dy',   ddt = x sum_n r B + sum_n A p,   dz = dy y' silu'(z).
-// The sums over channels are joined over the wave's lanes by merges (half the values move at each
-// step), over the four waves in shared memory, and over channel tiles by a second kernel.
-template <class T, int NP>
-__global__ __launch_bounds__(256) void sscan_bwd_kernel(ScanArgs a, int tiles) {
+// Halves keep the states and decays of 8 tokens in registers rather than 16 (64 values a lane less), for
+// the recurrence of the first 8 run twice. The sums over channels are joined over the wave's lanes by
+// merges (half the values move at each step), over the four waves in shared memory, and over
+// channel tiles by a second kernel.
+template <class T, int NP, bool GATE>
+__global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles) {
   typedef Lanes<NP> L;
+  constexpr int HT = TT / 2;
   constexpr int LEFT = L::LPC >= 16 ? 2 : 1;  // of 8 values, what a lane ends with: the wave has 64 / LPC channels
   __shared__ float2 sX[TT][L::CH];          // dt, dt x
   __shared__ float sG[TT][L::CH];           // dy'; then sum_n r B
-  __shared__ float sP[TT][L::CH];           // y without the gate; then sum_n A p
+  __shared__ float sP[TT][L::CH];           // sum_n A p
+  __shared__ float sY[GATE ? TT : 1][L::CH];  // y without skip and gate
   __shared__ float sB[TT][NP], sC[TT][NP];
-  __shared__ float sS[4][TT][2 * NP];       // a wave's dC (first NP), dB
-  const int per = a.D / a.G;
+  // a wave's dC (first NP), dB; behind them a place for the lanes that end with half sums
+  __shared__ float sS[L::LPC <= 4 ? 8 : 4][TT][2 * NP];
+  __shared__ float sBias[L::CH], sSkip[L::CH];
   const int bx = blockIdx.x % (a.G * tiles), grp = bx / tiles, tile = bx % tiles;
   const int c0 = tile * L::CH;
-  const Segment sg = segment_at(a, blockIdx.x / (a.G * tiles));
+  const Segment sg = segment_at(a.sq, blockIdx.x / (a.G * tiles), a.seg, a.segoff);
+  Stage<T, NP> sv(a, grp, c0);
   const int tid = threadIdx.x, part = tid % L::LPC, chl = tid / L::LPC, lane = tid % 64, wave = tid / 64;
-  const bool in = c0 + chl < per;
-  const int64_t d = (int64_t)grp * per + c0 + chl;
-  const bool vec = a.vec != 0;
-  float A[NPL], q[NPL], dA[NPL];
+  const bool in = c0 + chl < sv.per;
+  const int64_t d = (int64_t)grp * sv.per + c0 + chl;
+  float A[NPL], A2[NPL], q[NPL], dA[NPL];
   load_states<NP>(a.A, d, a.N, part, in, A);
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) q[i] = dA[i] = 0.f;
+  for (int i = 0; i < NPL; ++i) {
+    A2[i] = A[i] * kLog2e;
+    q[i] = dA[i] = 0.f;
+  }
   if (a.dfinal != nullptr) load_states<NP>(a.dfinal, (int64_t)sg.n * a.D + d, a.N, part, in, q);
-  if (in)
-    for (int64_t s = sg.first + sg.count - 1; s > sg.first + sg.j; --s) {
-      const float sum = a.seg_dt[s * a.D + d];
-      const float4 loc = *reinterpret_cast<const float4*>(a.seg_state + (s * a.D + d) * NP + part * NPL);
-      const float add[NPL] = {loc.x, loc.y, loc.z, loc.w};
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) q[i] = fmaf(exp2_hw(sum * (A[i] * kLog2e)), q[i], add[i]);
-    }
-  float bias[L::ITEMS][4], skip[L::ITEMS][4], dskip[L::ITEMS][4], dbias[L::ITEMS][4];
+  if (in && a.split) {
+    const int64_t count = segments_of(seq_end(a.sq, sg.n) - seq_begin(a.sq, sg.n), a.lseg);
+    join_segments<NP>(a, first_local(a, sg.n) + count - 1, -1, count - (int64_t)(sg.j + 1) * (a.seg / a.lseg), d, part, A2, q);
+  }
+  const int64_t chunk0 = first_chunk(a, sg);
+  sv.params(a.dt_bias, sBias);
+  sv.params(a.skip, sSkip);
+  // where a lane's sum over channels goes: bit 5 dC or dB, bits 4 and 3 the state of its four
+  float* to = &sS[L::LPC <= 4 && (lane & 7) >= L::LPC ? 4 + wave : wave][0]
+                 [(lane >> 5) * NP + part * NPL + ((lane >> 4) & 1) * 2 + (LEFT == 1 ? (lane >> 3) & 1 : 0)];
+  float dskip[L::ITEMS][4], dbias[L::ITEMS][4];
   Vec<T, 4> rx[L::ITEMS], rd[L::ITEMS], rz[L::ITEMS], ry[L::ITEMS];
   T rb[L::BCI], rc[L::BCI];
   float nh[NPL];
+  uint32_t ox[L::ITEMS], od[L::ITEMS], oz[L::ITEMS], oy[L::ITEMS], ob[L::BCI], oc[L::BCI];
 #pragma unroll
   for (int k = 0; k < L::ITEMS; ++k) {
-    const int pc = c0 + (tid + k * 256) % L::Q * 4;
+    ox[k] = sv.offset(k, a.x_row);
+    od[k] = sv.offset(k, a.dt_row);
+    oz[k] = sv.offset(k, a.z_row);
+    oy[k] = sv.offset(k, a.D);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const bool ok = tid + k * 256 < TT * L::Q && pc + e < per;
-      bias[k][e] = ok && a.dt_bias != nullptr ? a.dt_bias[(int64_t)grp * per + pc + e] : 0.f;
-      skip[k][e] = ok && a.skip != nullptr ? a.skip[(int64_t)grp * per + pc + e] : 0.f;
-      dskip[k][e] = dbias[k][e] = 0.f;
-    }
+    for (int e = 0; e < 4; ++e) dskip[k][e] = dbias[k][e] = 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < L::BCI; ++k) {
+    ob[k] = sv.bc_offset(k, a.b_row, a.N);
+    oc[k] = sv.bc_offset(k, a.c_row, a.N);
   }
   auto fetch = [&](int at) {
+    const int64_t t = sg.t0 + at;
+    const int live = sg.len - at;
 #pragma unroll
     for (int k = 0; k < L::ITEMS; ++k) {
-      const int p = tid + k * 256, pt = at + p / L::Q, pc = c0 + p % L::Q * 4;
-      const int valid = p < TT * L::Q && pt < sg.len ? per - pc : 0;
-      const int64_t t = sg.t0 + pt, col = (int64_t)grp * per + pc;
-      rx[k] = load_n<T, 4>(static_cast<const T*>(a.x) + t * a.x_row + col, valid, vec);
-      rd[k] = load_n<T, 4>(static_cast<const T*>(a.dt) + t * a.dt_row + col, valid, vec);
-      ry[k] = load_n<T, 4>(static_cast<const T*>(a.dy) + t * a.D + col, valid, vec);
-      if (a.z != nullptr) rz[k] = load_n<T, 4>(static_cast<const T*>(a.z) + t * a.z_row + col, valid, vec);
+      rx[k] = sv.load(a.x, t, a.x_row, ox[k], k, live);
+      rd[k] = sv.load(a.dt, t, a.dt_row, od[k], k, live);
+      ry[k] = sv.load(a.dy, t, a.D, oy[k], k, live);
+      if (GATE) rz[k] = sv.load(a.z, t, a.z_row, oz[k], k, live);
     }
 #pragma unroll
     for (int k = 0; k < L::BCI; ++k) {
-      const int p = tid + k * 256, pt = at + p / NP, n = p % NP;
-      const bool ok = p < TT * NP && pt < sg.len && n < a.N;
-      const int64_t t = sg.t0 + pt;
-      rb[k] = ok ? static_cast<const T*>(a.B)[t * a.b_row + (int64_t)grp * a.N + n] : (T)0.f;
-      rc[k] = ok ? static_cast<const T*>(a.C)[t * a.c_row + (int64_t)grp * a.N + n] : (T)0.f;
+      rb[k] = sv.load_bc(a.B, t, a.b_row, ob[k], k, a.N, live);
+      rc[k] = sv.load_bc(a.C, t, a.c_row, oc[k], k, a.N, live);
     }
-    load_states<NP>(a.states, (sg.chunk0 + at / TT) * a.D + d, a.N, part, in, nh);
+    load_states<NP>(a.states, (chunk0 + at / TT) * a.D + d, a.N, part, in, nh);
   };
   const int last = (sg.len - 1) / TT * TT;
   if (sg.len > 0) fetch(last);
+  __syncthreads();
   for (int at = last; at >= 0 && sg.len > 0; at -= TT) {
+    sv.renew();
+    const int live = sg.len - at;
     Vec<T, 4> kx[L::ITEMS], kd[L::ITEMS], kz[L::ITEMS], ky[L::ITEMS];
-    float hs[TT + 1][NPL], as[TT][NPL];
+    float h0[NPL], dAc[NPL];
 #pragma unroll
     for (int k = 0; k < L::ITEMS; ++k) {
-      const int p = tid + k * 256, pt = p / L::Q;
       kx[k] = rx[k];
       kd[k] = rd[k];
       kz[k] = rz[k];
       ky[k] = ry[k];
-      if (p < TT * L::Q) {
-        const bool live = at + pt < sg.len;
+      if (sv.has(k)) {
+        const bool ok = sv.token(k) < live;
+        float bias[4], g4[4];
+        unpack(*reinterpret_cast<const float4*>(&sBias[sv.col(k)]), bias);
+        float2* to = &sX[sv.token(k)][sv.col(k)];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float dt = as_f(rd[k].v[e]) + bias[k][e];
+          float dt = as_f(rd[k].v[e]) + bias[e];
           if (a.softplus) dt = softplus(dt);
-          dt = live ? dt : 0.f;
-          float g = as_f(ry[k].v[e]);
-          if (a.z != nullptr) {
+          dt = ok ? dt : 0.f;
+          g4[e] = as_f(ry[k].v[e]);
+          if (GATE) {
             const float z = as_f(rz[k].v[e]);
-            g *= z * sigmoid(z);
+            g4[e] *= z * sigmoid(z);
           }
-          sX[pt][p % L::Q * 4 + e] = make_float2(dt, dt * as_f(rx[k].v[e]));
-          sG[pt][p % L::Q * 4 + e] = g;
+          to[e] = make_float2(dt, dt * as_f(rx[k].v[e]));
         }
+        *reinterpret_cast<float4*>(&sG[sv.token(k)][sv.col(k)]) = make_float4(g4[0], g4[1], g4[2], g4[3]);
       }
     }
 #pragma unroll
-    for (int k = 0; k < L::BCI; ++k) {
-      const int p = tid + k * 256;
-      if (p < TT * NP) {
-        sB[p / NP][p % NP] = as_f(rb[k]);
-        sC[p / NP][p % NP] = as_f(rc[k]);
+    for (int k = 0; k < L::BCI; ++k)
+      if (sv.bc_has(k)) {
+        sB[sv.bc_token(k)][sv.bc_state(k)] = as_f(rb[k]);
+        sC[sv.bc_token(k)][sv.bc_state(k)] = as_f(rc[k]);
       }
-    }
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) hs[0][i] = nh[i];
+    for (int i = 0; i < NPL; ++i) {
+      h0[i] = nh[i];
+      dAc[i] = 0.f;
+    }
     __syncthreads();
     if (at > 0) fetch(at - TT);
+    for (int half = 1; half >= 0; --half) {
+      float hs[HT + 1][NPL], as[HT][NPL];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const float2 v = sX[t][chl];
-      const float4 b4 = *reinterpret_cast<const float4*>(&sB[t][part * NPL]);
-      const float bb[NPL] = {b4.x, b4.y, b4.z, b4.w};
+      for (int i = 0; i < NPL; ++i) hs[0][i] = h0[i];
+      if (half == 1) {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        as[t][i] = exp2_hw(v.x * (A[i] * kLog2e));
-        hs[t + 1][i] = fmaf(as[t][i], hs[t][i], v.y * bb[i]);
-      }
-      if (a.z != nullptr) {
-        const float4 c4 = *reinterpret_cast<const float4*>(&sC[t][part * NPL]);
-        float y = fmaf(c4.x, hs[t + 1][0], fmaf(c4.y, hs[t + 1][1], fmaf(c4.z, hs[t + 1][2], c4.w * hs[t + 1][3])));
-        y = group_sum<L::LPC>(y);
-        if (part == 0) sP[t][chl] = y;
-      }
-    }
-    if (a.z != nullptr) {
-      // dz needs y before sP is used again
-      __syncthreads();
+        for (int t = 0; t < HT; ++t) {
+          const float2 v = sX[t][chl];
+          float bb[NPL];
+          unpack(*reinterpret_cast<const float4*>(&sB[t][part * NPL]), bb);
 #pragma unroll
-      for (int k = 0; k < L::ITEMS; ++k) {
-        const int p = tid + k * 256, pt = p / L::Q, pc = p % L::Q * 4;
-        if (p < TT * L::Q && at + pt < sg.len) {
-          float out[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float z = as_f(kz[k].v[e]), s = sigmoid(z);
-            out[e] = as_f(ky[k].v[e]) * fmaf(skip[k][e], as_f(kx[k].v[e]), sP[pt][pc + e]) * (s * (1.f + z * (1.f - s)));
-          }
-          if (a.dz != nullptr)
-            store_n<T, 4>(static_cast<T*>(a.dz) + (sg.t0 + at + pt) * a.D + (int64_t)grp * per + c0 + pc, out, per - c0 - pc, vec);
+          for (int i = 0; i < NPL; ++i) hs[0][i] = fmaf(exp2_hw(v.x * A2[i]), hs[0][i], v.y * bb[i]);
         }
       }
-      __syncthreads();
-    }
-    float dAc[NPL];
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) dAc[i] = 0.f;
+      for (int u = 0; u < HT; ++u) {
+        const int t = half * HT + u;
+        const float2 v = sX[t][chl];
+        float bb[NPL];
+        unpack(*reinterpret_cast<const float4*>(&sB[t][part * NPL]), bb);
 #pragma unroll
-    for (int t = TT - 1; t >= 0; --t) {
-      const float2 v = sX[t][chl];
-      const float g = sG[t][chl];
-      const float4 b4 = *reinterpret_cast<const float4*>(&sB[t][part * NPL]);
-      const float4 c4 = *reinterpret_cast<const float4*>(&sC[t][part * NPL]);
-      const float bb[NPL] = {b4.x, b4.y, b4.z, b4.w}, cc[NPL] = {c4.x, c4.y, c4.z, c4.w};
-      float s1 = 0.f, s2 = 0.f, val[8];
+        for (int i = 0; i < NPL; ++i) {
+          as[u][i] = exp2_hw(v.x * A2[i]);
+          hs[u + 1][i] = fmaf(as[u][i], hs[u][i], v.y * bb[i]);
+        }
+        if (GATE) {
+          float cc[NPL];
+          unpack(*reinterpret_cast<const float4*>(&sC[t][part * NPL]), cc);
+          float y = cc[0] * hs[u + 1][0];
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const float r = fmaf(cc[i], g, q[i]);
-        val[i] = g * hs[t + 1][i];
-        val[4 + i] = r * v.y;
-        s1 = fmaf(r, bb[i], s1);
-        q[i] = as[t][i] * r;
-        const float p = q[i] * hs[t][i];
-        s2 = fmaf(p, A[i], s2);
-        dAc[i] = fmaf(p, v.x, dAc[i]);
+          for (int i = 1; i < NPL; ++i) y = fmaf(cc[i], hs[u + 1][i], y);
+          y = group_sum<L::LPC>(y);
+          sY[t][chl] = y;  // the same from all lanes of the channel
+        }
       }
-      s1 = group_sum<L::LPC>(s1);
-      s2 = group_sum<L::LPC>(s2);
-      if (part == 0) {
-        sG[t][chl] = s1;  // this lane group alone reads and writes its channel's place
-        sP[t][chl] = s2;
-      }
-      // val[0..3]: dC, val[4..7]: dB of this lane's four states; lanes of the wave with the same part
-      // hold the other channels
-      float m4[4], m2[2];
+      // The reverse walk loads B, C, dt and dt x again: without the opaque copies of the indexes the compiler
+      // would keep them from the walk above, 80 registers a lane. A token's loads are issued one ahead.
+      int rch = chl, rpart = part;
+      asm volatile("" : "+v"(rch), "+v"(rpart));
+      float2 nv = sX[half * HT + HT - 1][rch];
+      float ng = sG[half * HT + HT - 1][rch];
+      float4 nb = *reinterpret_cast<const float4*>(&sB[half * HT + HT - 1][rpart * NPL]);
+      float4 nc = *reinterpret_cast<const float4*>(&sC[half * HT + HT - 1][rpart * NPL]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) m4[i] = merge<32>(val[i], val[4 + i], lane);   // bit 5: dC or dB
+      for (int u = HT - 1; u >= 0; --u) {
+        const int t = half * HT + u;
+        const float2 v = nv;
+        const float g = ng;
+        float bb[NPL], cc[NPL];
+        unpack(nb, bb);
+        unpack(nc, cc);
+        if (u > 0) {
+          nv = sX[t - 1][rch];
+          ng = sG[t - 1][rch];
+          nb = *reinterpret_cast<const float4*>(&sB[t - 1][rpart * NPL]);
+          nc = *reinterpret_cast<const float4*>(&sC[t - 1][rpart * NPL]);
+        }
+        float s1 = 0.f, s2 = 0.f, val[8];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) m2[i] = merge<16>(m4[i], m4[2 + i], lane);     // bit 4: states 0, 1 or 2, 3
-      const int kind = lane >> 5, pair = (lane >> 4) & 1;
-      float* to = &sS[wave][t][kind * NP + part * NPL + pair * 2];
-      if constexpr (LEFT == 2) {
-        // LPC = 16: two values left, every lane's own
-        to[0] = m2[0];
-        to[1] = m2[1];
-      } else {
-        float m = merge<8>(m2[0], m2[1], lane);                                  // bit 3: the one or the other
-        if constexpr (L::LPC <= 4) m += xor_lane<4>(m);
-        if constexpr (L::LPC <= 2) m += xor_lane<2>(m);
-        if constexpr (L::LPC <= 1) m += xor_lane<1>(m);
-        if ((lane & 7) < L::LPC) to[(lane >> 3) & 1] = m;
+        for (int i = 0; i < NPL; ++i) {
+          const float r = fmaf(cc[i], g, q[i]);
+          val[i] = g * hs[u + 1][i];
+          val[4 + i] = r * v.y;
+          s1 = fmaf(r, bb[i], s1);
+          q[i] = as[u][i] * r;
+          const float p = q[i] * hs[u][i];
+          s2 = fmaf(p, A[i], s2);
+          dAc[i] = fmaf(p, v.x, dAc[i]);
+        }
+        s1 = group_sum<L::LPC>(s1);
+        s2 = group_sum<L::LPC>(s2);
+        sG[t][rch] = s1;  // only this channel's lanes, all of this wave, have read the place
+        sP[t][rch] = s2;
+        // val[0..3]: dC, val[4..7]: dB of this lane's four states; lanes of the wave with the same part
+        // hold the other channels
+        float m4[4], m2[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m4[i] = merge<32>(val[i], val[4 + i], lane);   // bit 5: dC or dB
+#pragma unroll
+        for (int i = 0; i < 2; ++i) m2[i] = merge<16>(m4[i], m4[2 + i], lane);     // bit 4: states 0, 1 or 2, 3
+        if constexpr (LEFT == 2) {
+          // LPC = 16: two values left, every lane's own
+          to[t * 2 * NP] = m2[0];
+          to[t * 2 * NP + 1] = m2[1];
+        } else {
+          float m = merge<8>(m2[0], m2[1], lane);                                  // bit 3: the one or the other
+          if constexpr (L::LPC <= 2) m += dpp<kXor2>(m);
+          if constexpr (L::LPC <= 4) m += dpp<kShl4>(m);                           // whole where bit 2 is clear
+          to[t * 2 * NP] = m;
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < NPL; ++i) dA[i] += dAc[i];
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < L::ITEMS; ++k) {
-      const int p = tid + k * 256, pt = p / L::Q, pc = p % L::Q * 4;
-      if (p < TT * L::Q && at + pt < sg.len) {
-        float ox[4], od[4];
+    for (int k = 0; k < L::ITEMS; ++k)
+      if (sv.has(k)) {
+        const int pt = sv.token(k), pc = sv.col(k);
+        float vx[4], vd[4], vz[4], s1[4], s2[4], y[4], skip[4], bias[4];
+        unpack(*reinterpret_cast<const float4*>(&sG[pt][pc]), s1);
+        unpack(*reinterpret_cast<const float4*>(&sP[pt][pc]), s2);
+        unpack(*reinterpret_cast<const float4*>(&sSkip[pc]), skip);
+        unpack(*reinterpret_cast<const float4*>(&sBias[pc]), bias);
+        if (GATE) unpack(*reinterpret_cast<const float4*>(&sY[pt][pc]), y);
+        const bool ok = pt < live;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float raw = as_f(kd[k].v[e]) + bias[k][e], x = as_f(kx[k].v[e]);
+          const float x = as_f(kx[k].v[e]);
           float g = as_f(ky[k].v[e]);
-          if (a.z != nullptr) {
-            const float z = as_f(kz[k].v[e]);
-            g *= z * sigmoid(z);
+          if (GATE) {
+            const float z = as_f(kz[k].v[e]), s = sigmoid(z);
+            vz[e] = g * fmaf(skip[e], x, y[e]) * (s * fmaf(z, 1.f - s, 1.f));
+            g *= z * s;
           }
-          const float s1 = sG[pt][pc + e];
-          ox[e] = fmaf(sX[pt][pc + e].x, s1, skip[k][e] * g);
-          od[e] = fmaf(x, s1, sP[pt][pc + e]);
-          if (a.softplus) od[e] *= sigmoid(raw);
+          vx[e] = fmaf(sX[pt][pc + e].x, s1[e], skip[e] * g);
+          vd[e] = fmaf(x, s1[e], s2[e]);
+          if (a.softplus) vd[e] *= sigmoid(as_f(kd[k].v[e]) + bias[e]);
           dskip[k][e] = fmaf(g, x, dskip[k][e]);
-          dbias[k][e] += od[e];
+          dbias[k][e] += ok ? vd[e] : 0.f;
         }
-        const int64_t o = (sg.t0 + at + pt) * a.D + (int64_t)grp * per + c0 + pc;
-        store_n<T, 4>(static_cast<T*>(a.dx) + o, ox, per - c0 - pc, vec);
-        store_n<T, 4>(static_cast<T*>(a.ddt) + o, od, per - c0 - pc, vec);
+        sv.store(a.dx, sg.t0 + at, a.D, oy[k], k, live, vx);
+        sv.store(a.ddt, sg.t0 + at, a.D, oy[k], k, live, vd);
+        if (a.dz != nullptr) sv.store(a.dz, sg.t0 + at, a.D, oy[k], k, live, vz);
       }
-    }
     for (int p = tid; p < TT * 2 * NP; p += 256) {
       const int pt = p / (2 * NP), v = p % (2 * NP);
-      if (at + pt < sg.len)
+      if (pt < live)
         a.part_bc[(((int64_t)tile * a.sq.total + sg.t0 + at + pt) * a.G + grp) * 2 * NP + v] =
             (sS[0][pt][v] + sS[1][pt][v]) + (sS[2][pt][v] + sS[3][pt][v]);
     }
@@ -596,22 +729,20 @@ __global__ __launch_bounds__(256) void sscan_bwd_kernel(ScanArgs a, int tiles) {
   const int64_t s = sg.first + sg.j;
   if (a.dh0 != nullptr && sg.j == 0) store_states<NP>(a.dh0, (int64_t)sg.n * a.D + d, a.N, part, in, q);
   if (in) *reinterpret_cast<float4*>(a.part_a + (s * a.D + d) * NP + part * NPL) = make_float4(dA[0], dA[1], dA[2], dA[3]);
-  // dskip and ddt_bias: the 16 (or fewer) threads that staged a channel join in shared memory
+  // dskip and ddt_bias: the 16 threads that staged a channel join in shared memory
   for (int which = 0; which < 2; ++which) {
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < L::ITEMS; ++k) {
-      const int p = tid + k * 256;
-      if (p < TT * L::Q)
+    for (int k = 0; k < L::ITEMS; ++k)
+      if (sv.has(k))
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sG[p / L::Q][p % L::Q * 4 + e] = which == 0 ? dskip[k][e] : dbias[k][e];
-    }
+        for (int e = 0; e < 4; ++e) sG[sv.token(k)][sv.col(k) + e] = which == 0 ? dskip[k][e] : dbias[k][e];
     __syncthreads();
-    if (tid < L::CH && c0 + tid < per) {
+    if (tid < L::CH && c0 + tid < sv.per) {
       float sum = 0.f;
 #pragma unroll
       for (int t = 0; t < TT; ++t) sum += sG[t][tid];
-      a.part_d[(s * 2 + which) * a.D + (int64_t)grp * per + c0 + tid] = sum;
+      a.part_d[(s * 2 + which) * a.D + (int64_t)grp * sv.per + c0 + tid] = sum;
     }
   }
 }
@@ -658,41 +789,39 @@ __global__ __launch_bounds__(256) void sscan_param_kernel(ScanArgs a, int NP) {
   }
 }
 
-// First segment and first chunk of each packed sequence.
-__global__ __launch_bounds__(1024) void sscan_tables_kernel(const int32_t* cu, int n, int seg, int32_t* segoff,
-                                                            int32_t* choff) {
-  __shared__ int sh[2][1024];
-  int base[2] = {0, 0};
+// First segment, first local segment and first chunk of each packed sequence.
+__global__ __launch_bounds__(1024) void sscan_tables_kernel(const int32_t* cu, int n, int seg, int lseg, int32_t* segoff,
+                                                            int32_t* loff, int32_t* choff) {
+  __shared__ int sh[3][1024];
+  int base[3] = {0, 0, 0};
+  int32_t* out[3] = {segoff, loff, choff};
   for (int i0 = 0; i0 < n; i0 += 1024) {
     const int i = i0 + threadIdx.x;
     const int len = i < n ? cu[i + 1] - cu[i] : 0;
-    const int mine[2] = {i < n ? max(1, (len + seg - 1) / seg) : 0, i < n ? (len + TT - 1) / TT : 0};
-    sh[0][threadIdx.x] = mine[0];
-    sh[1][threadIdx.x] = mine[1];
+    int mine[3] = {segments_of(len, seg), segments_of(len, lseg), (len + TT - 1) / TT};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if (i >= n) mine[k] = 0;
+      sh[k][threadIdx.x] = mine[k];
+    }
     __syncthreads();
     for (int step = 1; step < 1024; step *= 2) {
-      int add[2] = {0, 0};
-      if ((int)threadIdx.x >= step) {
-        add[0] = sh[0][threadIdx.x - step];
-        add[1] = sh[1][threadIdx.x - step];
-      }
+      int add[3];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) add[k] = (int)threadIdx.x >= step ? sh[k][threadIdx.x - step] : 0;
       __syncthreads();
-      sh[0][threadIdx.x] += add[0];
-      sh[1][threadIdx.x] += add[1];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) sh[k][threadIdx.x] += add[k];
       __syncthreads();
     }
-    if (i < n) {
-      segoff[i] = base[0] + sh[0][threadIdx.x] - mine[0];
-      choff[i] = base[1] + sh[1][threadIdx.x] - mine[1];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if (i < n) out[k][i] = base[k] + sh[k][threadIdx.x] - mine[k];
+      base[k] += sh[k][1023];
     }
-    base[0] += sh[0][1023];
-    base[1] += sh[1][1023];
     __syncthreads();
   }
-  if (threadIdx.x == 0) {
-    segoff[n] = base[0];
-    choff[n] = base[1];
-  }
+  if (threadIdx.x < 3) out[threadIdx.x][n] = base[threadIdx.x];
 }
 
 // One token: lanes as in the scan, the state read and written in place.
@@ -745,7 +874,8 @@ hipError_t fwd_np(const ScanArgs& a, hipStream_t st) {
   const int tiles = scan_tiles(a.D, a.N, a.G);
   const dim3 grid((unsigned)(a.nseg * a.G * tiles));
   if (a.split) {
-    hipLaunchKernelGGL((sscan_fwd_kernel<T, NP, false>), grid, dim3(256), 0, st, a, tiles);
+    const dim3 lgrid((unsigned)(a.nloc * a.G * tiles));
+    hipLaunchKernelGGL((sscan_fwd_kernel<T, NP, false>), lgrid, dim3(256), 0, st, a, tiles);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -759,10 +889,14 @@ hipError_t bwd_np(const ScanArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)(a.nseg * a.G * tiles));
   hipError_t e;
   if (a.split) {
-    hipLaunchKernelGGL((sscan_bwd_local_kernel<T, NP>), grid, dim3(256), 0, st, a, tiles);
+    const dim3 lgrid((unsigned)(a.nloc * a.G * tiles));
+    hipLaunchKernelGGL((sscan_bwd_local_kernel<T, NP>), lgrid, dim3(256), 0, st, a, tiles);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((sscan_bwd_kernel<T, NP>), grid, dim3(256), 0, st, a, tiles);
+  if (a.z != nullptr)
+    hipLaunchKernelGGL((sscan_bwd_kernel<T, NP, true>), grid, dim3(256), 0, st, a, tiles);
+  else
+    hipLaunchKernelGGL((sscan_bwd_kernel<T, NP, false>), grid, dim3(256), 0, st, a, tiles);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int64_t bc = a.sq.total * a.G * a.N;
   if (bc > 0) {
@@ -804,21 +938,30 @@ int scan_tiles(int D, int N, int G) {
   return (D / G + ch - 1) / ch;
 }
 
-// Tokens of a segment: a cut into about four workgroups a CU (forward) or two (backward, whose
-// registers allow no more), none shorter than 64 tokens. Where the longest sequence is at most two
-// such segments nothing is cut: the pass that a cut needs costs more than the fuller grid gives.
-int scan_seg(const Seqs& s, int64_t longest, int D, int N, int G, bool bwd) {
+// Tokens of a segment and of a local one: a cut into about four workgroups a CU (forward) or two
+// (backward, whose registers allow no more), none shorter than 64 tokens. Where the longest sequence is
+// at most two such segments nothing is cut: the pass that a cut needs costs more than the fuller
+// grid gives. Local segments: as short as keeps the first pass within eight workgroups a CU.
+void scan_seg(const Seqs& s, int64_t longest, int D, int N, int G, bool bwd, int* seg, int* lseg) {
   const int64_t cols = (int64_t)G * scan_tiles(D, N, G);
   const int64_t whole = longest > 0 ? (longest + kScanChunk - 1) / kScanChunk * kScanChunk : kScanChunk;
   const int64_t want = bwd ? 512 : 1024;
-  int64_t seg = (s.total * cols + want - 1) / want;
-  seg = (seg + kScanChunk - 1) / kScanChunk * kScanChunk;
-  if (seg < 64) seg = 64;
-  return (int)(whole <= 2 * seg ? whole : seg);
+  int64_t len = (s.total * cols + want - 1) / want;
+  len = (len + 63) / 64 * 64;
+  if (len < 64) len = 64;
+  if (whole <= 2 * len) {
+    *seg = *lseg = (int)whole;
+    return;
+  }
+  *seg = (int)len;
+  int r = 1;
+  while (r < 4 && (s.total / len + s.n) * cols * r * 2 <= 2048) r *= 2;
+  *lseg = (int)(len / r);
 }
 
-hipError_t launch_scan_tables(const Seqs& s, int seg, int32_t* segoff, int32_t* choff, hipStream_t st) {
-  hipLaunchKernelGGL(sscan_tables_kernel, dim3(1), dim3(1024), 0, st, s.cu, s.n, seg, segoff, choff);
+hipError_t launch_scan_tables(const Seqs& s, int seg, int lseg, int32_t* segoff, int32_t* loff, int32_t* choff,
+                              hipStream_t st) {
+  hipLaunchKernelGGL(sscan_tables_kernel, dim3(1), dim3(1024), 0, st, s.cu, s.n, seg, lseg, segoff, loff, choff);
   return hipGetLastError();
 }
 

@@ -64,9 +64,8 @@ __global__ __launch_bounds__(256) void kda_step_kernel(KdaStepArgs a, int vec) {
   }
 #pragma unroll
   for (int e = 0; e < 9; ++e) {
-    sum[e] += xor_lane<8>(sum[e]);
-    sum[e] += xor_lane<16>(sum[e]);
-    sum[e] += xor_lane<32>(sum[e]);
+    sum[e] += dpp<kRor8>(sum[e]);
+    sum[e] = add_xor32(add_xor16(sum[e]));
   }
   if (threadIdx.x % 64 < 8) {
 #pragma unroll
