@@ -137,11 +137,7 @@ kda_status conv_check(const kda_conv_dims* d, bool launching, Tokens* t, kda::Co
 // The backward's runs do not depend on what its pointers allow, so that the workspace has one size.
 size_t conv_bwd_ws(const kda_conv_dims* d, kda::ConvArgs* a) {
   a->tt = kda::conv_tile(a->sq.total, a->D, 4);
-  a->vec = 1;
-  const int64_t one = kda::conv_row_blocks(*a);
-  a->vec = 4;
-  const int64_t four = kda::conv_row_blocks(*a);
-  return align_up((size_t)(one > four ? one : four) * (d->W + 1) * d->D * sizeof(float));
+  return align_up((size_t)kda::conv_row_blocks(*a) * (d->W + 1) * d->D * sizeof(float));
 }
 
 }  // namespace
@@ -158,6 +154,7 @@ KDA_EXPORT kda_status kda_short_conv_fwd(const kda_conv_dims* dims, const void* 
   }
   a.x = x;
   a.w = weight;
+  a.wvec = reinterpret_cast<uintptr_t>(weight) % 16 == 0;
   a.bias = bias;
   a.h0 = h0;
   a.y = y;
@@ -192,6 +189,7 @@ KDA_EXPORT kda_status kda_short_conv_bwd(const kda_conv_dims* dims, const void* 
   TRY(check_ws(workspace, ws_bytes, conv_bwd_ws(dims, &a)));
   a.x = x;
   a.w = weight;
+  a.wvec = reinterpret_cast<uintptr_t>(weight) % 16 == 0;
   a.bias = bias;
   a.h0 = h0;
   a.dy = dy;
@@ -226,6 +224,7 @@ KDA_EXPORT kda_status kda_short_conv_step(const kda_conv_dims* dims, const void*
   a.x_row = c.x_row;
   a.x = x;
   a.w = weight;
+  a.wvec = reinterpret_cast<uintptr_t>(weight) % 16 == 0;
   a.bias = bias;
   a.slots = slots;
   a.state = state;

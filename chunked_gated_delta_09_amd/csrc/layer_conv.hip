@@ -9,28 +9,45 @@ namespace kda {
 
 namespace {
 
-// Tokens whose loads are issued together.
-constexpr int kAhead = 8;
+// Tokens whose loads are issued together, while the ones before them are worked on. A multiple of
+// every W (but 3), so that the windows need no moves between registers.
+constexpr int kAhead = 4;
+constexpr int kXcds = 8;
 
+// Workgroups go to the eight XCDs in turn. Neighbouring runs of tokens share the rows between them, so
+// each XCD, with its own L2, takes a stretch of neighbouring runs: n runs' blocks, this the i-th launched.
+__device__ __forceinline__ int64_t stretch_of(int64_t i, int64_t n) {
+  const int64_t q = n / kXcds, r = n % kXcds, x = i % kXcds;
+  return x * q + min(x, r) + i / kXcds;
+}
+
+// A wave has one run of tokens: its tokens and sequences are scalars.
 struct Cursor {
-  int n;               // sequence of the current token
-  int64_t begin, end;  // its tokens
+  int n;           // sequence of the current token
+  int begin, end;  // its tokens
 };
 
-__device__ __forceinline__ Cursor cursor_at(const Seqs& s, int64_t t) {
+__device__ __forceinline__ Cursor cursor_at(const Seqs& s, int t) {
   Cursor c;
   c.n = seq_of(s, t);
-  c.begin = seq_begin(s, c.n);
-  c.end = seq_end(s, c.n);
+  c.begin = (int)seq_begin(s, c.n);
+  c.end = (int)seq_end(s, c.n);
   return c;
 }
 // The next sequence that has a token (the caller's token t is one).
-__device__ __forceinline__ void advance(const Seqs& s, Cursor& c, int64_t t) {
+__device__ __forceinline__ void advance(const Seqs& s, Cursor& c, int t) {
   while (t >= c.end) {
     ++c.n;
     c.begin = c.end;
-    c.end = seq_end(s, c.n);
+    c.end = (int)seq_end(s, c.n);
   }
+}
+
+template <class T, int VEC>
+__device__ __forceinline__ void load_row(const void* p, int64_t at, int valid, float (&out)[VEC]) {
+  const auto v = load_n<T, VEC>(static_cast<const T*>(p) + at, valid, VEC > 1);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) out[e] = as_f(v.v[e]);
 }
 
 // Row r of a sequence's history [h0 | tokens] (r < W - 1: h0), for `ch` and VEC - 1 channels behind it.
@@ -38,39 +55,70 @@ template <class T, int W, int VEC>
 __device__ __forceinline__ void history_row(const ConvArgs& a, int n, int64_t begin, int64_t r, int ch, int valid,
                                             float (&out)[VEC]) {
   if (r >= W - 1) {
-    const auto v = load_n<T, VEC>(static_cast<const T*>(a.x) + (begin + r - (W - 1)) * a.x_row + ch, valid, VEC > 1);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) out[e] = as_f(v.v[e]);
+    load_row<T, VEC>(a.x, (begin + r - (W - 1)) * a.x_row + ch, valid, out);
   } else if (a.h0 != nullptr) {
-    const auto v = load_n<T, VEC>(static_cast<const T*>(a.h0) + ((int64_t)n * (W - 1) + r) * a.D + ch, valid, VEC > 1);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) out[e] = as_f(v.v[e]);
+    load_row<T, VEC>(a.h0, ((int64_t)n * (W - 1) + r) * a.D + ch, valid, out);
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) out[e] = 0.f;
   }
 }
 
+// The filters of VEC channels, VEC * W numbers in a row: 16 bytes a load where VEC > 1 (all channels
+// exist then) and the array is aligned.
 template <int W, int VEC>
-__device__ __forceinline__ void load_filter(const ConvArgs& a, int ch, float (&w)[W][VEC], float (&b)[VEC]) {
+__device__ __forceinline__ void load_filter(const float* weight, const float* bias, int wvec, int ch, float (&w)[W][VEC],
+                                            float (&b)[VEC]) {
+  float flat[VEC * W];
+  if (VEC > 1 && wvec) {
+    const float4* p = reinterpret_cast<const float4*>(weight + (int64_t)ch * W);
+#pragma unroll
+    for (int i = 0; i < VEC * W / 4; ++i) {
+      const float4 v = p[i];
+      flat[4 * i] = v.x;
+      flat[4 * i + 1] = v.y;
+      flat[4 * i + 2] = v.z;
+      flat[4 * i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC * W; ++i) flat[i] = weight[(int64_t)ch * W + i];
+  }
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
-    const bool in = ch + e < a.D;
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][e] = in ? a.w[(int64_t)(ch + e) * W + j] : 0.f;
-    b[e] = in && a.bias != nullptr ? a.bias[ch + e] : 0.f;
+    for (int j = 0; j < W; ++j) w[j][e] = flat[e * W + j];
+    b[e] = bias != nullptr ? bias[ch + e] : 0.f;
   }
 }
 
-// Grid: (token runs, then the sequences' final states) x channel blocks. Block: cx channel
-// threads x (256 / cx) runs.
+template <int W, int VEC>
+__device__ __forceinline__ void push(float (&win)[W][VEC], const float (&x)[VEC]) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) win[j][e] = win[j + 1][e];
+    win[W - 1][e] = x[e];
+  }
+}
+template <int W, int VEC>
+__device__ __forceinline__ float tap_sum(const float (&w)[W][VEC], const float (&win)[W][VEC], float b, int e) {
+  float u = b;
+#pragma unroll
+  for (int j = 0; j < W; ++j) u = fmaf(w[j][e], win[j][e], u);
+  return u;
+}
+
+// Grid: (runs of tokens, then the sequences' final states) x channel blocks. Block: cx channel
+// threads (whole waves) x 256 / cx runs.
 template <class T, int W, int VEC>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int cx, int64_t run_blocks) {
-  const int tx = threadIdx.x % cx, ty = threadIdx.x / cx, rows = 256 / cx;
+  const int tx = threadIdx.x % cx, rows = 256 / cx;
+  const int ty = __builtin_amdgcn_readfirstlane(threadIdx.x / cx);
   const int64_t rb = blockIdx.x;
   const int ch = (blockIdx.y * cx + tx) * VEC;
-  const int valid = a.D - ch;
-  if (valid <= 0) return;
+  if (ch >= a.D) return;
+  const int valid = VEC;  // D is a multiple of VEC
   if (rb >= run_blocks) {  // final state of `rows` sequences a block
     const int64_t n = (rb - run_blocks) * rows + ty;
     if (n >= a.sq.n) return;
@@ -83,41 +131,54 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int cx, int64
     }
     return;
   }
-  const int64_t t0 = (rb * rows + ty) * a.tt;
-  if (t0 >= a.sq.total) return;
-  const int64_t t1 = min(t0 + a.tt, a.sq.total);
+  const int64_t run = stretch_of(rb, run_blocks) * rows + ty;
+  if (run * a.tt >= a.sq.total) return;
+  const int t0 = (int)(run * a.tt), t1 = (int)min((int64_t)t0 + a.tt, a.sq.total);
+  const T* x = static_cast<const T*>(a.x);
+  T* y = static_cast<T*>(a.y);
+  Vec<T, VEC> next[kAhead];
+  auto fetch = [&](int t) {
+    if (t + kAhead <= t1) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) next[i] = load_n<T, VEC>(x + (t + i) * a.x_row + ch, valid, VEC > 1);
+    }
+  };
+  fetch(t0);
   float w[W][VEC], b[VEC], win[W][VEC];  // win[j]: the input of tap j
-  load_filter<W, VEC>(a, ch, w, b);
+  load_filter<W, VEC>(a.w, a.bias, a.wvec, ch, w, b);
   Cursor c = cursor_at(a.sq, t0);
 #pragma unroll
   for (int j = 1; j < W; ++j) history_row<T, W, VEC>(a, c.n, c.begin, t0 - c.begin + j - 1, ch, valid, win[j]);
-  const T* x = static_cast<const T*>(a.x);
-  T* y = static_cast<T*>(a.y);
-  for (int64_t t = t0; t < t1; t += kAhead) {
-    Vec<T, VEC> in[kAhead];
+  auto token = [&](const Vec<T, VEC>& in, int t) {
+    float v[VEC], out[VEC];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (t + i < t1) in[i] = load_n<T, VEC>(x + (t + i) * a.x_row + ch, valid, VEC > 1);
+    for (int e = 0; e < VEC; ++e) v[e] = as_f(in.v[e]);
+    push<W, VEC>(win, v);
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (t + i < t1) {
-        if (t + i >= c.end) {
-          advance(a.sq, c, t + i);
+    for (int e = 0; e < VEC; ++e) {
+      const float u = tap_sum<W, VEC>(w, win, b[e], e);
+      out[e] = a.act ? u * sigmoid(u) : u;
+    }
+    store_n<T, VEC>(y + (int64_t)t * a.D + ch, out, valid, VEC > 1);
+  };
+  for (int t = t0; t < t1; t += kAhead) {
+    if (t + kAhead <= min(t1, c.end)) {
+      Vec<T, VEC> in[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) in[i] = next[i];
+      fetch(t + kAhead);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) token(in[i], t + i);
+    } else {  // a sequence ends in these tokens, or the run does
+      fetch(t + kAhead);
+#pragma unroll 1
+      for (int s = t; s < min(t + kAhead, t1); ++s) {
+        if (s >= c.end) {
+          advance(a.sq, c, s);
 #pragma unroll
           for (int j = 1; j < W; ++j) history_row<T, W, VEC>(a, c.n, c.begin, j - 1, ch, valid, win[j]);
         }
-        float out[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-          for (int j = 0; j < W - 1; ++j) win[j][e] = win[j + 1][e];
-          win[W - 1][e] = as_f(in[i].v[e]);
-          float u = b[e];
-#pragma unroll
-          for (int j = 0; j < W; ++j) u = fmaf(w[j][e], win[j][e], u);
-          out[e] = a.act ? u * sigmoid(u) : u;
-        }
-        store_n<T, VEC>(y + (t + i) * a.D + ch, out, valid, VEC > 1);
+        token(load_n<T, VEC>(x + s * a.x_row + ch, valid, VEC > 1), s);
       }
     }
   }
@@ -126,22 +187,24 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int cx, int64
 // Backward of a run [t0, t1): du_t = dy_t act'(u_t) for its tokens and the W - 1 behind them (of
 // their sequence), each added into the pending dx of the W tokens that it saw; dx of a token is
 // whole once du of the token W - 1 behind it is in. The filter's gradient is summed over the run
-// in registers, over the block's runs in shared memory, and over blocks by a second kernel: one
+// in registers, over the block's four runs in shared memory, and over blocks by a second kernel: one
 // fixed order, no atomics.
 template <class T, int W, int VEC>
-__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int cx, int64_t run_blocks) {
-  extern __shared__ float sh[];  // [rows][W + 1][cx * VEC]
-  const int tx = threadIdx.x % cx, ty = threadIdx.x / cx, rows = 256 / cx;
+__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t run_blocks) {
+  __shared__ float sh[4][W + 1][64 * VEC];
+  const int tx = threadIdx.x % 64;
+  const int ty = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int64_t rb = blockIdx.x;
-  const int ch = (blockIdx.y * cx + tx) * VEC;
-  const int valid = a.D - ch;
+  const int ch = (blockIdx.y * 64 + tx) * VEC;
+  const bool inside = ch < a.D;
+  const int valid = VEC;  // D is a multiple of VEC
   const T* x = static_cast<const T*>(a.x);
   const T* dy = static_cast<const T*>(a.dy);
   float w[W][VEC], b[VEC];
-  if (valid > 0) load_filter<W, VEC>(a, ch, w, b);
-  if (rb >= run_blocks) {  // dh0 of `rows` sequences a block: history rows 0 .. W - 2
-    const int64_t n = (rb - run_blocks) * rows + ty;
-    if (n >= a.sq.n || valid <= 0) return;
+  if (inside) load_filter<W, VEC>(a.w, a.bias, a.wvec, ch, w, b);
+  if (rb >= run_blocks) {  // dh0 of four sequences a block: history rows 0 .. W - 2
+    const int64_t n = (rb - run_blocks) * 4 + ty;
+    if (n >= a.sq.n || !inside) return;
     const int64_t begin = seq_begin(a.sq, (int)n), len = seq_end(a.sq, (int)n) - begin;
     float acc[W - 1][VEC], win[W][VEC];
 #pragma unroll
@@ -149,26 +212,19 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int cx, int64
 #pragma unroll
       for (int e = 0; e < VEC; ++e) acc[i][e] = 0.f;
       history_row<T, W, VEC>(a, (int)n, begin, i, ch, valid, win[i + 1]);
-      if (a.dfinal != nullptr && i >= len) {
-        const auto d = load_n<T, VEC>(static_cast<const T*>(a.dfinal) + (n * (W - 1) + i - len) * a.D + ch, valid, VEC > 1);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[i][e] = as_f(d.v[e]);
-      }
+      if (a.dfinal != nullptr && i >= len) load_row<T, VEC>(a.dfinal, (n * (W - 1) + i - len) * a.D + ch, valid, acc[i]);
     }
 #pragma unroll
     for (int t = 0; t < W - 1; ++t) {
       if (t < len) {
-        const auto in = load_n<T, VEC>(x + (begin + t) * a.x_row + ch, valid, VEC > 1);
-        const auto g = load_n<T, VEC>(dy + (begin + t) * a.D + ch, valid, VEC > 1);
+        float in[VEC], g[VEC];
+        load_row<T, VEC>(x, (begin + t) * a.x_row + ch, valid, in);
+        load_row<T, VEC>(dy, (begin + t) * a.D + ch, valid, g);
+        push<W, VEC>(win, in);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-          for (int j = 0; j < W - 1; ++j) win[j][e] = win[j + 1][e];
-          win[W - 1][e] = as_f(in.v[e]);
-          float u = b[e];
-#pragma unroll
-          for (int j = 0; j < W; ++j) u = fmaf(w[j][e], win[j][e], u);
-          const float du = as_f(g.v[e]) * (a.act ? dact_f(u, KDA_ACT_SILU) : 1.f);
+          const float u = tap_sum<W, VEC>(w, win, b[e], e);
+          const float du = g[e] * (a.act ? dact_f(u, KDA_ACT_SILU) : 1.f);
 #pragma unroll
           for (int j = 0; j < W; ++j)
             if (t + j < W - 1) acc[t + j][e] = fmaf(w[j][e], du, acc[t + j][e]);
@@ -180,7 +236,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int cx, int64
       store_n<T, VEC>(static_cast<T*>(a.dh0) + (n * (W - 1) + i) * a.D + ch, acc[i], valid, VEC > 1);
     return;
   }
-  const int64_t t0 = (rb * rows + ty) * a.tt;
+  const int64_t run = stretch_of(rb, run_blocks) * 4 + ty;
   float dw[W][VEC], db[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
@@ -188,9 +244,22 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int cx, int64
 #pragma unroll
     for (int j = 0; j < W; ++j) dw[j][e] = 0.f;
   }
-  if (valid > 0 && t0 < a.sq.total) {
-    const int64_t t1 = min(t0 + a.tt, a.sq.total);
+  if (inside && run * a.tt < a.sq.total) {
+    const int t0 = (int)(run * a.tt), t1 = (int)min((int64_t)t0 + a.tt, a.sq.total);
+    const int t2 = (int)min((int64_t)t1 + W - 1, a.sq.total);
+    T* dx = static_cast<T*>(a.dx) + ch;
     float win[W][VEC], pend[W][VEC];  // pend[m]: dx so far of the token W - 1 - m before the current one
+    Vec<T, VEC> nx[kAhead], ng[kAhead];
+    auto fetch = [&](int t) {
+      if (t + kAhead <= t1) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          nx[i] = load_n<T, VEC>(x + (t + i) * a.x_row + ch, valid, VEC > 1);
+          ng[i] = load_n<T, VEC>(dy + (int64_t)(t + i) * a.D + ch, valid, VEC > 1);
+        }
+      }
+    };
+    fetch(t0);
     Cursor c = cursor_at(a.sq, t0);
 #pragma unroll
     for (int j = 1; j < W; ++j) history_row<T, W, VEC>(a, c.n, c.begin, t0 - c.begin + j - 1, ch, valid, win[j]);
@@ -198,88 +267,92 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int cx, int64
     for (int j = 0; j < W; ++j)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) pend[j][e] = 0.f;
-    // what dfinal adds to dx of token s: rows len .. len + W - 2 of the history are the final state
-    auto finish = [&](int64_t s, float (&v)[VEC]) {
-      if (a.dfinal != nullptr) {
-        Cursor f = s >= c.begin ? c : cursor_at(a.sq, s);
-        const int64_t i = (W - 1) - (f.end - s);
-        if (i >= 0) {
-          const auto d = load_n<T, VEC>(static_cast<const T*>(a.dfinal) + ((int64_t)f.n * (W - 1) + i) * a.D + ch, valid, VEC > 1);
+    const float zero[VEC] = {};
+    // du of one token; what it adds to the pending dx from tap `from` on (the taps before it are h0's)
+    auto token = [&](const Vec<T, VEC>& in, const Vec<T, VEC>& gin, int from, float mine) {
+      float v[VEC];
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) v[e] += as_f(d.v[e]);
-        }
+      for (int e = 0; e < VEC; ++e) v[e] = as_f(in.v[e]);
+      push<W, VEC>(win, v);
+      push<W, VEC>(pend, zero);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float u = tap_sum<W, VEC>(w, win, b[e], e);
+        const float du = as_f(gin.v[e]) * (a.act ? dact_f(u, KDA_ACT_SILU) : 1.f);
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+          if (j >= from) pend[j][e] = fmaf(w[j][e], du, pend[j][e]);
+        const float own = mine == 1.f ? du : 0.f;
+        db[e] += own;
+#pragma unroll
+        for (int j = 0; j < W; ++j) dw[j][e] = fmaf(own, win[j][e], dw[j][e]);
       }
-      store_n<T, VEC>(static_cast<T*>(a.dx) + s * a.D + ch, v, valid, VEC > 1);
     };
-    const int64_t t2 = min(t1 + W - 1, a.sq.total);
-    for (int64_t t = t0; t < t1 + W - 1; t += kAhead) {
-      Vec<T, VEC> in[kAhead], g[kAhead];
+    for (int t = t0; t < t1 + W - 1; t += kAhead) {
+      if (t - (W - 1) >= t0 && t - (W - 1) >= c.begin && t + kAhead + (W - 1) < c.end && t + kAhead <= t1) {
+        // inside the run, and the tokens that get whole are clear of both ends of the sequence
+        Vec<T, VEC> in[kAhead], g[kAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (t + i < t2) {
-          in[i] = load_n<T, VEC>(x + (t + i) * a.x_row + ch, valid, VEC > 1);
-          g[i] = load_n<T, VEC>(dy + (t + i) * a.D + ch, valid, VEC > 1);
+        for (int i = 0; i < kAhead; ++i) {
+          in[i] = nx[i];
+          g[i] = ng[i];
         }
+        fetch(t + kAhead);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int64_t s = t + i;
-        if (s < t1 + W - 1) {
+        for (int i = 0; i < kAhead; ++i) {
+          token(in[i], g[i], 0, 1.f);
+          store_n<T, VEC>(dx + (int64_t)(t + i - (W - 1)) * a.D, pend[0], valid, VEC > 1);
+        }
+      } else {
+        fetch(t + kAhead);
+#pragma unroll 1
+        for (int s = t; s < min(t + kAhead, t1 + W - 1); ++s) {
+          const int done = s - (W - 1);  // the token whose dx is whole after s
           if (s < t2) {
             if (s >= c.end) {
               advance(a.sq, c, s);
 #pragma unroll
               for (int j = 1; j < W; ++j) history_row<T, W, VEC>(a, c.n, c.begin, j - 1, ch, valid, win[j]);
             }
-            const int64_t pos = s - c.begin;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-              for (int j = 0; j < W - 1; ++j) {
-                win[j][e] = win[j + 1][e];
-                pend[j][e] = pend[j + 1][e];
-              }
-              win[W - 1][e] = as_f(in[i].v[e]);
-              pend[W - 1][e] = 0.f;
-              float u = b[e];
-#pragma unroll
-              for (int j = 0; j < W; ++j) u = fmaf(w[j][e], win[j][e], u);
-              const float du = as_f(g[i].v[e]) * (a.act ? dact_f(u, KDA_ACT_SILU) : 1.f);
-#pragma unroll
-              for (int j = 0; j < W; ++j)
-                if (pos >= W - 1 - j) pend[j][e] = fmaf(w[j][e], du, pend[j][e]);
-              if (s < t1) {
-                db[e] += du;
-#pragma unroll
-                for (int j = 0; j < W; ++j) dw[j][e] = fmaf(du, win[j][e], dw[j][e]);
-              }
-            }
+            token(load_n<T, VEC>(x + s * a.x_row + ch, valid, VEC > 1),
+                  load_n<T, VEC>(dy + (int64_t)s * a.D + ch, valid, VEC > 1), W - 1 - (s - c.begin), s < t1 ? 1.f : 0.f);
           } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-              for (int j = 0; j < W - 1; ++j) pend[j][e] = pend[j + 1][e];
-              pend[W - 1][e] = 0.f;
-            }
+            push<W, VEC>(pend, zero);
           }
-          if (s - (W - 1) >= t0 && s - (W - 1) < t1) finish(s - (W - 1), pend[0]);
+          if (done >= t0 && done < t1) {
+            float v[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) v[e] = pend[0][e];
+            if (a.dfinal != nullptr) {
+              // rows len .. len + W - 2 of the history are the final state
+              const Cursor f = done >= c.begin ? c : cursor_at(a.sq, done);
+              const int r = (W - 1) - (f.end - done);
+              if (r >= 0) {
+                float d[VEC];
+                load_row<T, VEC>(a.dfinal, ((int64_t)f.n * (W - 1) + r) * a.D + ch, valid, d);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) v[e] += d[e];
+              }
+            }
+            store_n<T, VEC>(dx + (int64_t)done * a.D, v, valid, VEC > 1);
+          }
         }
       }
     }
   }
-  // [rows][W + 1][cx * VEC] -> one row of partial sums a block
-  const int width = cx * VEC;
+  // one row of partial sums a block
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) sh[(ty * (W + 1) + j) * width + tx * VEC + e] = dw[j][e];
-    sh[(ty * (W + 1) + W) * width + tx * VEC + e] = db[e];
+    for (int j = 0; j < W; ++j) sh[ty][j][tx * VEC + e] = dw[j][e];
+    sh[ty][W][tx * VEC + e] = db[e];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < (W + 1) * width; i += 256) {
-    const int j = i / width, col = blockIdx.y * width + i % width;
-    float s = 0.f;
-    for (int r = 0; r < rows; ++r) s += sh[(r * (W + 1) + j) * width + i % width];
-    if (col < a.D) a.part[((int64_t)rb * (W + 1) + j) * a.D + col] = s;
+  for (int i = threadIdx.x; i < (W + 1) * 64 * VEC; i += 256) {
+    const int j = i / (64 * VEC), col = i % (64 * VEC);
+    if ((int)blockIdx.y * 64 * VEC + col < a.D)
+      a.part[((int64_t)rb * (W + 1) + j) * a.D + blockIdx.y * 64 * VEC + col] =
+          (sh[0][j][col] + sh[1][j][col]) + (sh[2][j][col] + sh[3][j][col]);
   }
 }
 
@@ -316,12 +389,12 @@ __global__ __launch_bounds__(1024) void conv_filter_kernel(ConvArgs a, int64_t b
 
 template <class T, int W, int VEC>
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepArgs a) {
-  const int b = blockIdx.y;
+  const int row = blockIdx.y;
   const int ch = (blockIdx.x * 256 + threadIdx.x) * VEC;
-  const int slot = step_slot(a.slots, b, a.slots_n);
-  const int valid = a.D - ch;
-  if (valid <= 0) return;
-  T* y = static_cast<T*>(a.y) + (int64_t)b * a.D + ch;
+  const int slot = step_slot(a.slots, row, a.slots_n);
+  if (ch >= a.D) return;
+  const int valid = VEC;  // D is a multiple of VEC
+  T* y = static_cast<T*>(a.y) + (int64_t)row * a.D + ch;
   float out[VEC];
   if (slot < 0) {
 #pragma unroll
@@ -333,14 +406,14 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepArgs a) {
   Vec<T, VEC> old[W - 1];
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) old[j] = load_n<T, VEC>(st + (int64_t)j * a.D, valid, VEC > 1);
-  const auto x = load_n<T, VEC>(static_cast<const T*>(a.x) + b * a.x_row + ch, valid, VEC > 1);
+  const auto x = load_n<T, VEC>(static_cast<const T*>(a.x) + row * a.x_row + ch, valid, VEC > 1);
+  float w[W][VEC], b[VEC];
+  load_filter<W, VEC>(a.w, a.bias, a.wvec, ch, w, b);
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
-    const bool in = e < valid;
-    float u = in && a.bias != nullptr ? a.bias[ch + e] : 0.f;
+    float u = b[e];
 #pragma unroll
-    for (int j = 0; j < W; ++j)
-      u = fmaf(in ? a.w[(int64_t)(ch + e) * W + j] : 0.f, as_f(j < W - 1 ? old[j < W - 1 ? j : 0].v[e] : x.v[e]), u);
+    for (int j = 0; j < W; ++j) u = fmaf(w[j][e], as_f(j < W - 1 ? old[j < W - 1 ? j : 0].v[e] : x.v[e]), u);
     out[e] = a.act ? u * sigmoid(u) : u;
   }
   store_n<T, VEC>(y, out, valid, VEC > 1);
@@ -353,16 +426,9 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepArgs a) {
   }
 }
 
-// Channel threads of a block: the power of two that covers the channels, up to `most`.
-int channel_threads(int D, int vec, int most) {
-  int cx = 1;
-  while (cx < most && cx * vec < D) cx *= 2;
-  return cx;
-}
-
 template <class T, int W>
 hipError_t fwd_w(const ConvArgs& a, hipStream_t st) {
-  const int cx = channel_threads(a.D, a.vec, 256), rows = 256 / cx;
+  const int cx = a.D <= 64 * a.vec ? 64 : 256, rows = 256 / cx;
   const int64_t runs = (a.sq.total + a.tt - 1) / a.tt, rb = (runs + rows - 1) / rows;
   const int64_t fb = a.final_state != nullptr ? (a.sq.n + rows - 1) / rows : 0;
   if (rb + fb == 0) return hipSuccess;
@@ -382,16 +448,14 @@ hipError_t fwd_w(const ConvArgs& a, hipStream_t st) {
 template <class T, int W>
 hipError_t bwd_w(const ConvArgs& a, hipStream_t st) {
   const int vec = a.vec > 1 ? 4 : 1;
-  const int cx = channel_threads(a.D, vec, 64), rows = 256 / cx;
   const int64_t rb = conv_row_blocks(a);
-  const int64_t hb = a.dh0 != nullptr ? (a.sq.n + rows - 1) / rows : 0;
-  const size_t lds = sizeof(float) * 256 * vec * (W + 1);
-  const dim3 grid((unsigned)(rb + hb), (a.D + cx * vec - 1) / (cx * vec));
+  const int64_t hb = a.dh0 != nullptr ? (a.sq.n + 3) / 4 : 0;
+  const dim3 grid((unsigned)(rb + hb), (a.D + 64 * vec - 1) / (64 * vec));
   if (rb + hb > 0) {
     if (vec == 4)
-      hipLaunchKernelGGL((conv_bwd_kernel<T, W, 4>), grid, dim3(256), lds, st, a, cx, rb);
+      hipLaunchKernelGGL((conv_bwd_kernel<T, W, 4>), grid, dim3(256), 0, st, a, rb);
     else
-      hipLaunchKernelGGL((conv_bwd_kernel<T, W, 1>), grid, dim3(256), lds, st, a, cx, rb);
+      hipLaunchKernelGGL((conv_bwd_kernel<T, W, 1>), grid, dim3(256), 0, st, a, rb);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -446,12 +510,7 @@ int conv_tile(int64_t total, int D, int vec) {
   return tt;
 }
 
-int64_t conv_row_blocks(const ConvArgs& a) {
-  const int vec = a.vec > 1 ? 4 : 1;
-  const int rows = 256 / channel_threads(a.D, vec, 64);
-  const int64_t runs = (a.sq.total + a.tt - 1) / a.tt;
-  return (runs + rows - 1) / rows;
-}
+int64_t conv_row_blocks(const ConvArgs& a) { return ((a.sq.total + a.tt - 1) / a.tt + 3) / 4; }
 
 hipError_t launch_conv_fwd(int dtype, const ConvArgs& a, hipStream_t st) { CONV_DISPATCH(fwd_w, a); }
 hipError_t launch_conv_bwd(int dtype, const ConvArgs& a, hipStream_t st) { CONV_DISPATCH(bwd_w, a); }

@@ -118,7 +118,7 @@ __device__ __forceinline__ int find_seq(const int32_t* first, int n, int64_t t) 
 __device__ __forceinline__ int64_t seq_begin(const Seqs& s, int n) { return s.cu ? s.cu[n] : (int64_t)n * s.T; }
 __device__ __forceinline__ int64_t seq_end(const Seqs& s, int n) { return s.cu ? s.cu[n + 1] : (int64_t)(n + 1) * s.T; }
 __device__ __forceinline__ int seq_of(const Seqs& s, int64_t t) {
-  return s.cu ? find_seq(s.cu, s.n, t) : (int)(t / s.T);
+  return s.cu ? find_seq(s.cu, s.n, t) : (int)((uint32_t)t / (uint32_t)s.T);  // tokens fit 31 bits
 }
 
 // The state row of batch row b in a token step: slots[b], or b itself without a table. A negative slot

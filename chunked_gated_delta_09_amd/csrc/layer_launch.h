@@ -28,6 +28,7 @@ struct ConvArgs {
   float* part;        // bwd: [row blocks][W + 1][D] sums of a block's tokens
   int tt;             // tokens that a thread walks
   int vec;            // 4 or 8 channels a thread, or 1 where the rows are not aligned for it
+  int wvec;           // weight is 16-byte aligned
 };
 int conv_vec(int dtype, int D, int64_t x_row, const void* const* ptrs, int np);
 int conv_tile(int64_t total, int D, int vec);
@@ -36,7 +37,7 @@ hipError_t launch_conv_fwd(int dtype, const ConvArgs& a, hipStream_t st);
 hipError_t launch_conv_bwd(int dtype, const ConvArgs& a, hipStream_t st);
 
 struct ConvStepArgs {
-  int B, D, W, act, slots_n;
+  int B, D, W, act, slots_n, wvec;
   int64_t x_row;
   const void* x;
   const float *w, *bias;
