@@ -533,6 +533,11 @@ int norm_vec(const kda::NormArgs& a, int dtype, const void* const* ptrs, int np)
   return ok;
 }
 
+// Weight and bias allow four-element loads: a group's first channel is on a multiple of four.
+int norm_wvec(const kda::NormArgs& a, const float* w, const float* b) {
+  return a.C % 4 == 0 && reinterpret_cast<uintptr_t>(w) % 16 == 0 && reinterpret_cast<uintptr_t>(b) % 16 == 0;
+}
+
 size_t norm_ws(const kda_norm_dims* d) {
   kda::NormPlan p;
   kda::norm_plan(d->dtype, d->R, d->G, d->C, d->shared, &p);
@@ -556,6 +561,7 @@ KDA_EXPORT kda_status kda_group_norm_fwd(const kda_norm_dims* dims, const void* 
   a.y = y;
   const void* p[3] = {x, gate, y};
   a.vec = norm_vec(a, dims->dtype, p, 3);
+  a.wvec = norm_wvec(a, weight, bias);
   return hip_status(kda::launch_norm_fwd(dims->dtype, a, static_cast<hipStream_t>(stream)), "kda_group_norm_fwd");
 }
 
@@ -591,6 +597,7 @@ KDA_EXPORT kda_status kda_group_norm_bwd(const kda_norm_dims* dims, const void* 
   a.part = sums ? static_cast<float*>(workspace) : nullptr;
   const void* p[5] = {x, gate, dy, dx, dgate};
   a.vec = norm_vec(a, dims->dtype, p, 5);
+  a.wvec = norm_wvec(a, weight, bias);
   return hip_status(kda::launch_norm_bwd(dims->dtype, a, static_cast<hipStream_t>(stream)), "kda_group_norm_bwd");
 }
 

@@ -18,16 +18,40 @@ struct alignas(sizeof(T) * N) Vec {
 __device__ __forceinline__ float as_f(bf16 x) { return (float)x; }
 __device__ __forceinline__ float as_f(float x) { return x; }
 
-// N elements at p, as floats; lanes take those below `valid`, zero behind. `vec`: p is aligned
-// for one load of all N.
+// N elements as loaded, in whole registers: two bf16 each (elements of their own would take a
+// register each wherever two ways of loading them meet).
 template <class T, int N>
-__device__ __forceinline__ Vec<T, N> load_n(const T* p, int valid, bool vec) {
-  Vec<T, N> r;
-  if (vec && valid >= N) {
-    r = *reinterpret_cast<const Vec<T, N>*>(p);
+struct Pack {
+  static constexpr int WORDS = (N * (int)sizeof(T) + 3) / 4;
+  uint32_t w[WORDS];
+  __device__ __forceinline__ float at(int e) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+    return __uint_as_float(e % 2 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+  }
+};
+
+// N elements at p; those from `valid` on are zero. `vec`: p is aligned for one load of all N.
+template <class T, int N>
+__device__ __forceinline__ Pack<T, N> load_n(const T* p, int valid, bool vec) {
+  Pack<T, N> r;
+  if (vec && valid >= N && N > 1) {
+    struct alignas(sizeof(T) * N < 4 ? 4 : sizeof(T) * N) Words {
+      uint32_t w[Pack<T, N>::WORDS];
+    };
+    const Words v = *reinterpret_cast<const Words*>(p);
+#pragma unroll
+    for (int i = 0; i < Pack<T, N>::WORDS; ++i) r.w[i] = v.w[i];
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) r.v[i] = i < valid ? p[i] : (T)0.f;
+    for (int i = 0; i < Pack<T, N>::WORDS; ++i) r.w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < valid) {
+        if constexpr (sizeof(T) == 4)
+          r.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        else
+          r.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i % 2));
+      }
   }
   return r;
 }

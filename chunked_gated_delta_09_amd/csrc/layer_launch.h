@@ -27,7 +27,7 @@ struct ConvArgs {
   float *dw, *db;
   float* part;        // bwd: [row blocks][W + 1][D] sums of a block's tokens
   int tt;             // tokens that a thread walks
-  int vec;            // 4 or 8 channels a thread, or 1 where the rows are not aligned for it
+  int vec;            // 4: rows are aligned for four elements a load; 1: they are not
   int wvec;           // weight is 16-byte aligned
 };
 int conv_vec(int dtype, int D, int64_t x_row, const void* const* ptrs, int np);
@@ -107,10 +107,11 @@ struct NormArgs {
   float *dw, *db;
   float* part;     // bwd [rows of sums][2][columns]
   int vec;         // rows allow vector loads
+  int wvec;        // weight and bias too
 };
 struct NormPlan {
   int tpi, nch, vec;       // lanes of a group, chunks a lane holds, elements of a chunk
-  int64_t blocks;          // bwd workgroups
+  int64_t blocks;          // workgroups
   int64_t part_rows;       // rows of partial sums
   int part_cols;           // columns of one of the two sums
 };

@@ -1,16 +1,16 @@
 // Norm per group of channels with an activation, forward and backward.
 //
 // A group's C channels are held in registers by tpi lanes (a power of two up to a wave, or a whole
-// workgroup), nch chunks of VEC elements each, so a row is read once: the mean, the centred sum of
-// squares and the output come from the registers. Bound by memory.
+// workgroup of 256 or 1024), one or two chunks of 16 bytes each, so a row is read once: the mean, the
+// centred sum of squares and the output come from the registers. Bound by memory.
 #include "layer_device.h"
 
 namespace kda {
 
 namespace {
 
-// Sum over the tpi lanes of a group. tpi = 256: the whole workgroup, through `sh` (4 floats; two
-// buffers alternate, so one barrier a sum is enough).
+// Sum over the tpi lanes of a group. tpi > 64: the whole workgroup, through `sh` (a float for each wave;
+// the sums of an item have places of their own, so one barrier a sum is enough).
 __device__ __forceinline__ float item_sum(float x, int tpi, float* sh) {
   if (tpi >= 2) x += dpp<kXor1>(x);
   if (tpi >= 4) x += dpp<kXor2>(x);
@@ -18,31 +18,47 @@ __device__ __forceinline__ float item_sum(float x, int tpi, float* sh) {
   if (tpi >= 16) x += dpp<kRor8>(x);
   if (tpi >= 32) x = add_xor16(x);
   if (tpi >= 64) x = add_xor32(x);
-  if (tpi == 256) {
+  if (tpi > 64) {
     if (threadIdx.x % 64 == 0) sh[threadIdx.x / 64] = x;
     __syncthreads();
-    x = (sh[0] + sh[1]) + (sh[2] + sh[3]);
+    x = 0.f;
+    for (int i = 0; i < tpi / 64; ++i) x += sh[i];
   }
   return x;
 }
 
+// A lane's share of a group, as loaded.
 template <class T, int VEC, int NCH>
-struct Row {
-  float v[NCH][VEC];
+struct Raw {
+  Pack<T, VEC> v[NCH];
+
+  __device__ __forceinline__ void load(const void* base, int64_t at, int C, int lane, int tpi, bool vec) {
+    const T* p = static_cast<const T*>(base) + at;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int col = (c * tpi + lane) * VEC;
+      v[c] = load_n<T, VEC>(p + col, C - col, vec);
+    }
+  }
+  __device__ __forceinline__ float at(int c, int e) const { return v[c].at(e); }
 };
 
-template <class T, int VEC, int NCH>
-__device__ __forceinline__ void load_row(const void* base, int64_t at, int C, int lane, int tpi, bool vec,
-                                         float (&out)[NCH][VEC]) {
-  const T* p = static_cast<const T*>(base) + at;
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int col = (c * tpi + lane) * VEC;
-    const auto r = load_n<T, VEC>(p + col, C - col, vec);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) out[c][e] = as_f(r.v[e]);
+// The activation of a call, without branches for its elements.
+struct Act {
+  bool none, silu;
+  __device__ __forceinline__ explicit Act(int act) : none(act == KDA_ACT_NONE), silu(act == KDA_ACT_SILU) {}
+  __device__ __forceinline__ float value(float x) const {
+    const float v = sigmoid(x) * (silu ? x : 1.f);
+    return none ? x : v;
   }
-}
+  // value and derivative
+  __device__ __forceinline__ float both(float x, float* d) const {
+    const float s = sigmoid(x), r = 1.f - s;
+    const float v = s * (silu ? x : 1.f), g = s * (silu ? fmaf(x, r, 1.f) : r);
+    *d = none ? 1.f : g;
+    return none ? x : v;
+  }
+};
 
 template <class T, int VEC, int NCH>
 __device__ __forceinline__ void store_row(void* base, int64_t at, int C, int lane, int tpi, bool vec,
@@ -56,15 +72,25 @@ __device__ __forceinline__ void store_row(void* base, int64_t at, int C, int lan
 }
 
 template <int VEC, int NCH>
-__device__ __forceinline__ void load_param(const float* p, float fill, int64_t at, int C, int lane, int tpi,
+__device__ __forceinline__ void load_param(const float* p, float fill, int64_t at, int C, int lane, int tpi, bool vec,
                                            float (&out)[NCH][VEC]) {
 #pragma unroll
-  for (int c = 0; c < NCH; ++c)
+  for (int c = 0; c < NCH; ++c) {
+    const int col = (c * tpi + lane) * VEC;
+    if (p != nullptr && vec && col + VEC <= C) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int col = (c * tpi + lane) * VEC + e;
-      out[c][e] = p != nullptr && col < C ? p[at + col] : fill;
+      for (int e = 0; e < VEC; e += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p + at + col + e);
+        out[c][e] = v.x;
+        out[c][e + 1] = v.y;
+        out[c][e + 2] = v.z;
+        out[c][e + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) out[c][e] = p != nullptr && col + e < C ? p[at + col + e] : fill;
     }
+  }
 }
 
 // x of a group -> n = (x - mean) rstd; returns rstd. Elements behind the group's end become zero.
@@ -91,7 +117,7 @@ __device__ __forceinline__ float normalise(const NormArgs& a, int lane, int tpi,
   for (int c = 0; c < NCH; ++c)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) q = fmaf(x[c][e], x[c][e], q);
-  const float rstd = 1.f / sqrtf(fmaf(item_sum(q, tpi, sh + 4), inv, a.eps));
+  const float rstd = 1.f / sqrtf(fmaf(item_sum(q, tpi, sh + 16), inv, a.eps));
 #pragma unroll
   for (int c = 0; c < NCH; ++c)
 #pragma unroll
@@ -99,91 +125,134 @@ __device__ __forceinline__ float normalise(const NormArgs& a, int lane, int tpi,
   return rstd;
 }
 
-template <class T, int VEC, int NCH>
-__global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a, int tpi) {
-  __shared__ float sh[8];
+// A group of lanes takes the items sub, sub + stride, ... with stride a multiple of G, so its channels
+// (and the weights in its registers) stay the same; the next item is loaded while this one is worked on.
+template <class T, int VEC, int NCH, int THREADS>
+__global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormArgs a, int tpi, int64_t stride) {
+  __shared__ float sh[32];
   const int lane = threadIdx.x % tpi;
-  const int64_t item = (int64_t)blockIdx.x * (256 / tpi) + threadIdx.x / tpi;
-  if (item >= a.R * a.G) return;  // whole groups of lanes leave; a workgroup-wide group always has its item
-  const int64_t row = item / a.G;
-  const int g = (int)(item % a.G);
+  const int64_t sub = (int64_t)blockIdx.x * (THREADS / tpi) + threadIdx.x / tpi;
+  const int64_t items = a.R * a.G;
+  if (sub >= items) return;  // whole groups of lanes leave; a workgroup-wide group always has its item
+  const int g = (int)(sub % a.G);
   const bool vec = a.vec != 0;
-  float x[NCH][VEC], gate[NCH][VEC], w[NCH][VEC], b[NCH][VEC];
-  load_row<T, VEC, NCH>(a.x, row * a.x_row + (int64_t)g * a.C, a.C, lane, tpi, vec, x);
-  if (a.gate != nullptr) load_row<T, VEC, NCH>(a.gate, row * a.gate_row + (int64_t)g * a.C, a.C, lane, tpi, vec, gate);
-  const int64_t pat = a.shared ? 0 : (int64_t)g * a.C;
-  load_param<VEC, NCH>(a.w, 1.f, pat, a.C, lane, tpi, w);
-  load_param<VEC, NCH>(a.bias, 0.f, pat, a.C, lane, tpi, b);
-  normalise<VEC, NCH>(a, lane, tpi, sh, x);
+  const int64_t pat = a.shared ? 0 : (int64_t)g * a.C, step = stride / a.G;
+  int64_t row = sub / a.G;
+  Raw<T, VEC, NCH> rx, rg;
+  rx.load(a.x, row * a.x_row + (int64_t)g * a.C, a.C, lane, tpi, vec);
+  if (a.gate != nullptr) rg.load(a.gate, row * a.gate_row + (int64_t)g * a.C, a.C, lane, tpi, vec);
+  float w[NCH][VEC], b[NCH][VEC];
+  load_param<VEC, NCH>(a.w, 1.f, pat, a.C, lane, tpi, a.wvec != 0, w);
+  load_param<VEC, NCH>(a.bias, 0.f, pat, a.C, lane, tpi, a.wvec != 0, b);
+  const Act act(a.act);
+  for (; row < a.R; row += step) {
+    float x[NCH][VEC];
+    const Raw<T, VEC, NCH> kg = rg;
 #pragma unroll
-  for (int c = 0; c < NCH; ++c)
+    for (int c = 0; c < NCH; ++c)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const float u = fmaf(x[c][e], w[c][e], b[c][e]);
-      x[c][e] = a.gate != nullptr ? u * act_f(gate[c][e], a.act) : act_f(u, a.act);
+      for (int e = 0; e < VEC; ++e) x[c][e] = rx.at(c, e);
+    if (row + step < a.R) {
+      rx.load(a.x, (row + step) * a.x_row + (int64_t)g * a.C, a.C, lane, tpi, vec);
+      if (a.gate != nullptr) rg.load(a.gate, (row + step) * a.gate_row + (int64_t)g * a.C, a.C, lane, tpi, vec);
     }
-  store_row<T, VEC, NCH>(a.y, item * a.C, a.C, lane, tpi, vec, x);
+    normalise<VEC, NCH>(a, lane, tpi, sh, x);
+    if (a.gate != nullptr) {
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[c][e] = fmaf(x[c][e], w[c][e], b[c][e]) * act.value(kg.at(c, e));
+    } else {
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[c][e] = act.value(fmaf(x[c][e], w[c][e], b[c][e]));
+    }
+    store_row<T, VEC, NCH>(a.y, (row * a.G + g) * a.C, a.C, lane, tpi, vec, x);
+    if (tpi > 64) __syncthreads();  // the sums' places are read before the next item's are written
+  }
 }
 
-// Backward. A group of lanes takes the items sub, sub + stride, ... with stride a multiple of G, so
-// its channels (and the weights in its registers) stay the same and dweight, dbias are summed in
-// registers. With du the gradient of u, dn = du w:
+// Backward, items dealt as above: dweight and dbias are summed in registers. With du the gradient of u, dn = du w:
 //   dx = rstd (dn - n mean(dn n) - [center] mean(dn)).
 // Partial sums: one row a group of lanes [sub][2][C], or with one weight for all groups one row a
 // workgroup.
-template <class T, int VEC, int NCH>
-__global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a, int tpi, int64_t stride) {
-  extern __shared__ float sh[];  // 16 floats, then [256 / tpi][C] where weights are shared
-  const int lane = threadIdx.x % tpi, subs = 256 / tpi;
+template <class T, int VEC, int NCH, int THREADS>
+__global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormArgs a, int tpi, int64_t stride) {
+  extern __shared__ float sh[];  // 64 floats, then [groups of lanes][C] where weights are shared
+  const int lane = threadIdx.x % tpi, subs = THREADS / tpi;
   const int64_t sub = (int64_t)blockIdx.x * subs + threadIdx.x / tpi;
   const int g = (int)(sub % a.G);
   const bool vec = a.vec != 0;
-  const int64_t items = a.R * a.G;
+  const int64_t items = a.R * a.G, step = stride / a.G;
   const float inv = 1.f / (float)a.C;
   float w[NCH][VEC], b[NCH][VEC], dw[NCH][VEC], db[NCH][VEC];
   const int64_t pat = a.shared ? 0 : (int64_t)g * a.C;
-  load_param<VEC, NCH>(a.w, 1.f, pat, a.C, lane, tpi, w);
-  load_param<VEC, NCH>(a.bias, 0.f, pat, a.C, lane, tpi, b);
+  int64_t row = sub / a.G;
+  Raw<T, VEC, NCH> rx, rg, rd;
+  auto fetch = [&](int64_t r) {
+    rx.load(a.x, r * a.x_row + (int64_t)g * a.C, a.C, lane, tpi, vec);
+    rd.load(a.dy, (r * a.G + g) * a.C, a.C, lane, tpi, vec);
+    if (a.gate != nullptr) rg.load(a.gate, r * a.gate_row + (int64_t)g * a.C, a.C, lane, tpi, vec);
+  };
+  if (sub < items) fetch(row);
+  load_param<VEC, NCH>(a.w, 1.f, pat, a.C, lane, tpi, a.wvec != 0, w);
+  load_param<VEC, NCH>(a.bias, 0.f, pat, a.C, lane, tpi, a.wvec != 0, b);
+  const Act act(a.act);
 #pragma unroll
   for (int c = 0; c < NCH; ++c)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dw[c][e] = db[c][e] = 0.f;
-  for (int64_t item = sub; item < items; item += stride) {
-    const int64_t row = item / a.G;
-    float x[NCH][VEC], gate[NCH][VEC], dy[NCH][VEC];
-    load_row<T, VEC, NCH>(a.x, row * a.x_row + (int64_t)g * a.C, a.C, lane, tpi, vec, x);
-    load_row<T, VEC, NCH>(a.dy, item * a.C, a.C, lane, tpi, vec, dy);
-    if (a.gate != nullptr) load_row<T, VEC, NCH>(a.gate, row * a.gate_row + (int64_t)g * a.C, a.C, lane, tpi, vec, gate);
+  for (; row < a.R; row += step) {
+    float x[NCH][VEC], dn[NCH][VEC];
+    const Raw<T, VEC, NCH> kd = rd, kg = rg;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[c][e] = rx.at(c, e);
+    if (row + step < a.R) fetch(row + step);
     const float rstd = normalise<VEC, NCH>(a, lane, tpi, sh, x);
+    const int64_t out = (row * a.G + g) * a.C;
     float s1 = 0.f, s2 = 0.f;
+    if (a.gate != nullptr) {
+      float dg[NCH][VEC];
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          float d;
+          const float dy = kd.at(c, e), v = act.both(kg.at(c, e), &d);
+          dg[c][e] = dy * fmaf(x[c][e], w[c][e], b[c][e]) * d;
+          dn[c][e] = dy * v;
+        }
+      store_row<T, VEC, NCH>(a.dgate, out, a.C, lane, tpi, vec, dg);
+    } else {
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          float d;
+          act.both(fmaf(x[c][e], w[c][e], b[c][e]), &d);
+          dn[c][e] = kd.at(c, e) * d;
+        }
+    }
 #pragma unroll
     for (int c = 0; c < NCH; ++c)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float u = fmaf(x[c][e], w[c][e], b[c][e]);
-        float du;
-        if (a.gate != nullptr) {
-          const float z = gate[c][e];
-          gate[c][e] = dy[c][e] * u * dact_f(z, a.act);
-          du = dy[c][e] * act_f(z, a.act);
-        } else {
-          du = dy[c][e] * dact_f(u, a.act);
-        }
-        db[c][e] += du;
-        dw[c][e] = fmaf(du, x[c][e], dw[c][e]);
-        const float dn = du * w[c][e];
-        dy[c][e] = dn;
-        s1 += dn;
-        s2 = fmaf(dn, x[c][e], s2);
+        db[c][e] += dn[c][e];
+        dw[c][e] = fmaf(dn[c][e], x[c][e], dw[c][e]);
+        dn[c][e] *= w[c][e];
+        s1 += dn[c][e];
+        s2 = fmaf(dn[c][e], x[c][e], s2);
       }
-    if (a.gate != nullptr) store_row<T, VEC, NCH>(a.dgate, item * a.C, a.C, lane, tpi, vec, gate);
-    s1 = a.center ? item_sum(s1, tpi, sh + 8) * inv : 0.f;
-    s2 = item_sum(s2, tpi, sh + 12) * inv;
+    s1 = a.center ? item_sum(s1, tpi, sh + 32) * inv : 0.f;
+    s2 = item_sum(s2, tpi, sh + 48) * inv;
 #pragma unroll
     for (int c = 0; c < NCH; ++c)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) x[c][e] = rstd * (dy[c][e] - s1 - x[c][e] * s2);
-    store_row<T, VEC, NCH>(a.dx, item * a.C, a.C, lane, tpi, vec, x);
+      for (int e = 0; e < VEC; ++e) x[c][e] = rstd * (dn[c][e] - s1 - x[c][e] * s2);
+    store_row<T, VEC, NCH>(a.dx, out, a.C, lane, tpi, vec, x);
   }
   if (a.part == nullptr) return;
   if (!a.shared || subs == 1) {
@@ -202,7 +271,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a, int tpi, int6
       }
     return;
   }
-  float* acc = sh + 16;
+  float* acc = sh + 64;
   for (int k = 0; k < 2; ++k) {
     __syncthreads();
 #pragma unroll
@@ -213,7 +282,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a, int tpi, int6
         if (col < a.C) acc[(threadIdx.x / tpi) * a.C + col] = k == 0 ? dw[c][e] : db[c][e];
       }
     __syncthreads();
-    for (int col = threadIdx.x; col < a.C; col += 256) {
+    for (int col = threadIdx.x; col < a.C; col += THREADS) {
       float s = 0.f;
       for (int r = 0; r < subs; ++r) s += acc[r * a.C + col];
       a.part[((int64_t)blockIdx.x * 2 + k) * a.C + col] = s;
@@ -249,46 +318,50 @@ __global__ __launch_bounds__(1024) void col_sum_kernel(const float* in, int64_t 
   }
 }
 
-template <class T, int VEC, int NCH>
+template <class T, int VEC, int NCH, int THREADS>
 hipError_t norm_fwd_t(const NormArgs& a, const NormPlan& p, hipStream_t st) {
-  const int subs = 256 / p.tpi;
-  const int64_t blocks = (a.R * a.G + subs - 1) / subs;
-  hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, NCH>), dim3((unsigned)blocks), dim3(256), 0, st, a, p.tpi);
+  hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, NCH, THREADS>), dim3((unsigned)p.blocks), dim3(THREADS), 0, st, a, p.tpi,
+                     p.blocks * (THREADS / p.tpi));
   return hipGetLastError();
 }
 
-template <class T, int VEC, int NCH>
+template <class T, int VEC, int NCH, int THREADS>
 hipError_t norm_bwd_t(const NormArgs& a, const NormPlan& p, hipStream_t st) {
-  const int subs = 256 / p.tpi;
-  const size_t lds = sizeof(float) * (16 + (a.shared && subs > 1 ? (size_t)subs * a.C : 0));
-  hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, NCH>), dim3((unsigned)p.blocks), dim3(256), lds, st, a, p.tpi,
+  const int subs = THREADS / p.tpi;
+  const size_t lds = sizeof(float) * (64 + (a.shared && subs > 1 ? (size_t)subs * a.C : 0));
+  hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, NCH, THREADS>), dim3((unsigned)p.blocks), dim3(THREADS), lds, st, a, p.tpi,
                      p.blocks * subs);
   return hipGetLastError();
 }
 
-#define NORM_DISPATCH(FN, T, VEC)                      \
-  switch (p.nch) {                                     \
-    case 1: return FN<T, VEC, 1>(a, p, st);            \
-    case 2: return FN<T, VEC, 2>(a, p, st);            \
-    case 4: return FN<T, VEC, 4>(a, p, st);            \
-    default: return FN<T, VEC, 8>(a, p, st);           \
-  }
+// A bf16 group of 1024 lanes never needs a second chunk: 8192 channels are one each.
+#define NORM_DISPATCH(FN)                                                    \
+  do {                                                                       \
+    if (dtype == KDA_F32) {                                                  \
+      if (p.tpi == 1024)                                                     \
+        return p.nch == 1 ? FN<float, 4, 1, 1024>(a, p, st) : FN<float, 4, 2, 1024>(a, p, st); \
+      return p.nch == 1 ? FN<float, 4, 1, 256>(a, p, st) : FN<float, 4, 2, 256>(a, p, st);     \
+    }                                                                        \
+    if (p.tpi == 1024) return FN<bf16, 8, 1, 1024>(a, p, st);                \
+    return p.nch == 1 ? FN<bf16, 8, 1, 256>(a, p, st) : FN<bf16, 8, 2, 256>(a, p, st);         \
+  } while (0)
 
 }  // namespace
 
-// Lanes of a group: enough for one chunk of 16 bytes each up to a wave, two chunks a lane up to
-// 2 waves' worth, then the whole workgroup. Backward workgroups: about eight a CU, a whole number of
-// rows' groups together (the lanes of a group stay on its channels), none without an item.
+// Lanes of a group: enough for one chunk of 16 bytes each up to a wave, for two chunks up to two waves'
+// worth, then a workgroup of 256 and of 1024 in the same way. Workgroups: about eight a CU of 256, a
+// whole number of rows' groups together (the lanes of a group stay on its channels), none without an
+// item.
 bool norm_plan(int dtype, int64_t R, int G, int C, int shared, NormPlan* p) {
   p->vec = dtype == KDA_F32 ? 4 : 8;
   const int chunks = (C + p->vec - 1) / p->vec;
   p->tpi = 1;
   while (p->tpi < 64 && p->tpi < chunks) p->tpi *= 2;
   if (chunks > 128) p->tpi = 256;
-  p->nch = 1;
-  while (p->nch * p->tpi < chunks) p->nch *= 2;
-  if (p->nch > 8) return false;
-  const int64_t subs = 256 / p->tpi;
+  if (chunks > 512) p->tpi = 1024;
+  p->nch = chunks > p->tpi ? 2 : 1;
+  if (chunks > 2 * p->tpi) return false;
+  const int64_t subs = p->tpi == 1024 ? 1 : 256 / p->tpi;
   // workgroups in steps of G / gcd(G, subs)
   int64_t g = G, h = subs;
   while (h) {
@@ -297,8 +370,9 @@ bool norm_plan(int dtype, int64_t R, int G, int C, int shared, NormPlan* p) {
     h = r;
   }
   const int64_t step = G / g;
+  const int64_t full = p->tpi == 1024 ? 512 : 2048;
   const int64_t most = (R * G + subs - 1) / subs;
-  int64_t blocks = (2048 + step - 1) / step * step;
+  int64_t blocks = (full + step - 1) / step * step;
   if (blocks > most) blocks = (most + step - 1) / step * step;
   p->blocks = blocks;
   p->part_cols = shared ? C : G * C;
@@ -310,18 +384,12 @@ hipError_t launch_norm_fwd(int dtype, const NormArgs& a, hipStream_t st) {
   if (a.R == 0) return hipSuccess;
   NormPlan p;
   norm_plan(dtype, a.R, a.G, a.C, a.shared, &p);
-  if (dtype == KDA_F32) {
-    NORM_DISPATCH(norm_fwd_t, float, 4);
-  }
-  NORM_DISPATCH(norm_fwd_t, bf16, 8);
+  NORM_DISPATCH(norm_fwd_t);
 }
 
 namespace {
 hipError_t norm_bwd_main(int dtype, const NormArgs& a, const NormPlan& p, hipStream_t st) {
-  if (dtype == KDA_F32) {
-    NORM_DISPATCH(norm_bwd_t, float, 4);
-  }
-  NORM_DISPATCH(norm_bwd_t, bf16, 8);
+  NORM_DISPATCH(norm_bwd_t);
 }
 }  // namespace
 

@@ -151,11 +151,11 @@ struct Stage {
     return (uint32_t)((bc_token(k) * row + (int64_t)grp * N + bc_state(k)) * (int64_t)sizeof(T));
   }
   // piece k of the chunk whose first token is t and that has `live` tokens
-  __device__ __forceinline__ Vec<T, 4> load(const void* p, int64_t t, int64_t row, uint32_t off, int k, int live) const {
+  __device__ __forceinline__ Pack<T, 4> load(const void* p, int64_t t, int64_t row, uint32_t off, int k, int live) const {
     const T* q = reinterpret_cast<const T*>(static_cast<const char*>(p) + t * row * (int64_t)sizeof(T) + off);
     if (inner && live >= TT) {
-      if (has(k)) return *reinterpret_cast<const Vec<T, 4>*>(q);
-      return Vec<T, 4>{};
+      if (has(k)) return load_n<T, 4>(q, 4, true);
+      return Pack<T, 4>{};
     }
     return load_n<T, 4>(q, has(k) && token(k) < live ? per - c0 - col(k) : 0, inner);
   }
@@ -236,7 +236,7 @@ __global__ __launch_bounds__(256) void sscan_fwd_kernel(ScanArgs a, int tiles) {
   sv.params(a.dt_bias, sBias);
   if (OUT) sv.params(a.skip, sSkip);
 
-  Vec<T, 4> rx[L::ITEMS], rd[L::ITEMS], rz[L::ITEMS];
+  Pack<T, 4> rx[L::ITEMS], rd[L::ITEMS], rz[L::ITEMS];
   T rb[L::BCI], rc[L::BCI];
   uint32_t ox[L::ITEMS], od[L::ITEMS], oz[L::ITEMS], oy[L::ITEMS], ob[L::BCI], oc[L::BCI];
 #pragma unroll
@@ -271,7 +271,7 @@ __global__ __launch_bounds__(256) void sscan_fwd_kernel(ScanArgs a, int tiles) {
   for (int at = 0; at < sg.len; at += TT) {
     sv.renew();
     const int live = sg.len - at;
-    Vec<T, 4> kx[L::ITEMS], kz[L::ITEMS];  // this chunk's, for its outputs
+    Pack<T, 4> kx[L::ITEMS], kz[L::ITEMS];  // this chunk's, for its outputs
 #pragma unroll
     for (int k = 0; k < L::ITEMS; ++k) {
       kx[k] = rx[k];
@@ -284,11 +284,11 @@ __global__ __launch_bounds__(256) void sscan_fwd_kernel(ScanArgs a, int tiles) {
         float2* to = &sX[sv.token(k)][sv.col(k)];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float dt = as_f(rd[k].v[e]) + bias[e];
+          float dt = rd[k].at(e) + bias[e];
           if (a.softplus) dt = softplus(dt);
           dt = ok ? dt : 0.f;
           if (!OUT) total[k][e] += dt;
-          to[e] = make_float2(dt, dt * as_f(rx[k].v[e]));
+          to[e] = make_float2(dt, dt * rx[k].at(e));
         }
       }
     }
@@ -327,9 +327,9 @@ __global__ __launch_bounds__(256) void sscan_fwd_kernel(ScanArgs a, int tiles) {
           unpack(*reinterpret_cast<const float4*>(&sY[sv.token(k)][sv.col(k)]), out);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            out[e] = fmaf(skip[e], as_f(kx[k].v[e]), out[e]);
+            out[e] = fmaf(skip[e], kx[k].at(e), out[e]);
             if (a.z != nullptr) {
-              const float z = as_f(kz[k].v[e]);
+              const float z = kz[k].at(e);
               out[e] *= z * sigmoid(z);
             }
           }
@@ -373,7 +373,7 @@ __global__ __launch_bounds__(256) void sscan_bwd_local_kernel(ScanArgs a, int ti
   }
   float total[L::ITEMS][4] = {};
   sv.params(a.dt_bias, sBias);
-  Vec<T, 4> rd[L::ITEMS], rz[L::ITEMS], ry[L::ITEMS];
+  Pack<T, 4> rd[L::ITEMS], rz[L::ITEMS], ry[L::ITEMS];
   T rc[L::BCI];
   uint32_t od[L::ITEMS], oz[L::ITEMS], oy[L::ITEMS], oc[L::BCI];
 #pragma unroll
@@ -411,13 +411,13 @@ __global__ __launch_bounds__(256) void sscan_bwd_local_kernel(ScanArgs a, int ti
         float2* to = &sX[sv.token(k)][sv.col(k)];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float dt = as_f(rd[k].v[e]) + bias[e];
+          float dt = rd[k].at(e) + bias[e];
           if (a.softplus) dt = softplus(dt);
           dt = ok ? dt : 0.f;
           total[k][e] += dt;
-          float g = as_f(ry[k].v[e]);
+          float g = ry[k].at(e);
           if (a.z != nullptr) {
-            const float z = as_f(rz[k].v[e]);
+            const float z = rz[k].at(e);
             g *= z * sigmoid(z);
           }
           to[e] = make_float2(dt, g);
@@ -511,7 +511,7 @@ __global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles
   float* to = &sS[L::LPC <= 4 && (lane & 7) >= L::LPC ? 4 + wave : wave][0]
                  [(lane >> 5) * NP + part * NPL + ((lane >> 4) & 1) * 2 + (LEFT == 1 ? (lane >> 3) & 1 : 0)];
   float dskip[L::ITEMS][4], dbias[L::ITEMS][4];
-  Vec<T, 4> rx[L::ITEMS], rd[L::ITEMS], rz[L::ITEMS], ry[L::ITEMS];
+  Pack<T, 4> rx[L::ITEMS], rd[L::ITEMS], rz[L::ITEMS], ry[L::ITEMS];
   T rb[L::BCI], rc[L::BCI];
   float nh[NPL];
   uint32_t ox[L::ITEMS], od[L::ITEMS], oz[L::ITEMS], oy[L::ITEMS], ob[L::BCI], oc[L::BCI];
@@ -552,7 +552,7 @@ __global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles
   for (int at = last; at >= 0 && sg.len > 0; at -= TT) {
     sv.renew();
     const int live = sg.len - at;
-    Vec<T, 4> kx[L::ITEMS], kd[L::ITEMS], kz[L::ITEMS], ky[L::ITEMS];
+    Pack<T, 4> kx[L::ITEMS], kd[L::ITEMS], kz[L::ITEMS], ky[L::ITEMS];
     float h0[NPL], dAc[NPL];
 #pragma unroll
     for (int k = 0; k < L::ITEMS; ++k) {
@@ -567,15 +567,15 @@ __global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles
         float2* to = &sX[sv.token(k)][sv.col(k)];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float dt = as_f(rd[k].v[e]) + bias[e];
+          float dt = rd[k].at(e) + bias[e];
           if (a.softplus) dt = softplus(dt);
           dt = ok ? dt : 0.f;
-          g4[e] = as_f(ry[k].v[e]);
+          g4[e] = ry[k].at(e);
           if (GATE) {
-            const float z = as_f(rz[k].v[e]);
+            const float z = rz[k].at(e);
             g4[e] *= z * sigmoid(z);
           }
-          to[e] = make_float2(dt, dt * as_f(rx[k].v[e]));
+          to[e] = make_float2(dt, dt * rx[k].at(e));
         }
         *reinterpret_cast<float4*>(&sG[sv.token(k)][sv.col(k)]) = make_float4(g4[0], g4[1], g4[2], g4[3]);
       }
@@ -701,16 +701,16 @@ __global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles
         const bool ok = pt < live;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float x = as_f(kx[k].v[e]);
-          float g = as_f(ky[k].v[e]);
+          const float x = kx[k].at(e);
+          float g = ky[k].at(e);
           if (GATE) {
-            const float z = as_f(kz[k].v[e]), s = sigmoid(z);
+            const float z = kz[k].at(e), s = sigmoid(z);
             vz[e] = g * fmaf(skip[e], x, y[e]) * (s * fmaf(z, 1.f - s, 1.f));
             g *= z * s;
           }
           vx[e] = fmaf(sX[pt][pc + e].x, s1[e], skip[e] * g);
           vd[e] = fmaf(x, s1[e], s2[e]);
-          if (a.softplus) vd[e] *= sigmoid(as_f(kd[k].v[e]) + bias[e]);
+          if (a.softplus) vd[e] *= sigmoid(kd[k].at(e) + bias[e]);
           dskip[k][e] = fmaf(g, x, dskip[k][e]);
           dbias[k][e] += ok ? vd[e] : 0.f;
         }

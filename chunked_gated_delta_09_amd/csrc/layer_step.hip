@@ -35,7 +35,7 @@ __global__ __launch_bounds__(256) void kda_step_kernel(KdaStepArgs a, int vec) {
   const T* k = static_cast<const T*>(a.k) + ((int64_t)b * a.H + h) * a.K;
   const float* g = a.g + ((int64_t)b * a.HV + hv) * a.K;
   float s[KI][4], kk[KI];
-  Vec<float, 4> raw[KI];
+  Pack<float, 4> raw[KI];
 #pragma unroll
   for (int i = 0; i < KI; ++i) {
     const int r = rg + i * kRowGroups;
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(256) void kda_step_kernel(KdaStepArgs a, int vec) {
     sum[8] = fmaf(qq, kk[i], sum[8]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      s[i][e] = decay * raw[i].v[e];
+      s[i][e] = decay * raw[i].at(e);
       sum[e] = fmaf(kk[i], s[i][e], sum[e]);
       sum[4 + e] = fmaf(qq, s[i][e], sum[4 + e]);
     }
@@ -77,7 +77,7 @@ __global__ __launch_bounds__(256) void kda_step_kernel(KdaStepArgs a, int vec) {
   float u[4], out[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    u[e] = beta * (as_f(v4.v[e]) - sum[e]);
+    u[e] = beta * (v4.at(e) - sum[e]);
     out[e] = a.scale * fmaf(sum[8], u[e], sum[4 + e]);
   }
   if (rg == 0 && valid > 0) store_n<T, 4>(o, out, valid, vec != 0);
