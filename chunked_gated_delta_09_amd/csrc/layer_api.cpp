@@ -540,7 +540,7 @@ int norm_wvec(const kda::NormArgs& a, const float* w, const float* b) {
 
 size_t norm_ws(const kda_norm_dims* d) {
   kda::NormPlan p;
-  kda::norm_plan(d->dtype, d->R, d->G, d->C, d->shared, &p);
+  kda::norm_plan(d->dtype, d->R, d->G, d->C, d->shared, true, &p);
   return align_up((size_t)p.part_rows * 2 * p.part_cols * sizeof(float));
 }
 

@@ -70,6 +70,20 @@ __device__ __forceinline__ void store_n(T* p, const float (&x)[N], int valid, bo
   }
 }
 
+// Four fp32 values of a state that a token step passes through once: past the caches, which hold
+// nothing of it by the next step. On the KDA step of 256 sequences x 32 heads of 128 x 128 (1.07 GB in
+// place) 207 us, against 258 through them; 4.0 against 4.4 us for one sequence of 16 heads.
+__device__ __forceinline__ float4 load_stream(const float* p) {
+  typedef float f4 __attribute__((ext_vector_type(4)));
+  const f4 v = __builtin_nontemporal_load(reinterpret_cast<const f4*>(p));
+  return make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store_stream(float* p, float4 v) {
+  typedef float f4 __attribute__((ext_vector_type(4)));
+  const f4 w = {v.x, v.y, v.z, v.w};
+  __builtin_nontemporal_store(w, reinterpret_cast<f4*>(p));
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // 2^x by the hardware instruction (results below the normal range become zero).

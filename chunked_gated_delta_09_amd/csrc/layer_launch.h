@@ -115,7 +115,7 @@ struct NormPlan {
   int64_t part_rows;       // rows of partial sums
   int part_cols;           // columns of one of the two sums
 };
-bool norm_plan(int dtype, int64_t R, int G, int C, int shared, NormPlan* p);
+bool norm_plan(int dtype, int64_t R, int G, int C, int shared, bool bwd, NormPlan* p);
 hipError_t launch_norm_fwd(int dtype, const NormArgs& a, hipStream_t st);
 hipError_t launch_norm_bwd(int dtype, const NormArgs& a, hipStream_t st);
 
@@ -129,8 +129,5 @@ struct KdaStepArgs {
   void* o;
 };
 hipError_t launch_kda_step(int dtype, const KdaStepArgs& a, hipStream_t st);
-
-// out[c] = sum over rows of in[r][c], rows in a fixed order (stride in elements between rows)
-hipError_t launch_col_sum(const float* in, int64_t rows, int64_t cols, int64_t stride, float* out, hipStream_t st);
 
 }  // namespace kda

@@ -290,31 +290,32 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormArgs a, int tpi, 
   }
 }
 
-// out[c] = sum_r in[r * stride + c]: 64 columns a workgroup, the rows dealt to 16 lanes a column
-// (four running sums each) and joined in order.
-__global__ __launch_bounds__(1024) void col_sum_kernel(const float* in, int64_t rows, int64_t cols, int64_t stride,
-                                                       float* out) {
-  __shared__ float sh[16][65];
-  const int tx = threadIdx.x % 64, ty = threadIdx.x / 64;
-  const int64_t col = (int64_t)blockIdx.x * 64 + tx;
+// out0[c], out1[c] = sum_r in[r][0][c], in[r][1][c]: 16 columns a workgroup, the rows dealt to 64 lanes a
+// column (four running sums each) and joined in a fixed order.
+__global__ __launch_bounds__(1024) void col_sum_kernel(const float* in, int64_t rows, int64_t cols, float* out0,
+                                                       float* out1) {
+  __shared__ float sh[64][17];
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const int64_t col = (int64_t)blockIdx.x * 16 + tx, stride = 2 * cols;
   float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-  if (col < cols) {
+  if (col < stride) {
     int64_t r = ty;
-    for (; r + 48 < rows; r += 64) {
+    for (; r + 192 < rows; r += 256) {
       s0 += in[r * stride + col];
-      s1 += in[(r + 16) * stride + col];
-      s2 += in[(r + 32) * stride + col];
-      s3 += in[(r + 48) * stride + col];
+      s1 += in[(r + 64) * stride + col];
+      s2 += in[(r + 128) * stride + col];
+      s3 += in[(r + 192) * stride + col];
     }
-    for (; r < rows; r += 16) s0 += in[r * stride + col];
+    for (; r < rows; r += 64) s0 += in[r * stride + col];
   }
   sh[ty][tx] = (s0 + s1) + (s2 + s3);
-  __syncthreads();
-  if (ty == 0 && col < cols) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s += sh[i][tx];
-    out[col] = s;
+  for (int half = 32; half > 0; half /= 2) {
+    __syncthreads();
+    if (ty < half) sh[ty][tx] += sh[ty + half][tx];
+  }
+  if (ty == 0 && col < stride) {
+    float* out = col < cols ? out0 : out1;
+    if (out != nullptr) out[col < cols ? col : col - cols] = sh[0][tx];
   }
 }
 
@@ -349,10 +350,10 @@ hipError_t norm_bwd_t(const NormArgs& a, const NormPlan& p, hipStream_t st) {
 }  // namespace
 
 // Lanes of a group: enough for one chunk of 16 bytes each up to a wave, for two chunks up to two waves'
-// worth, then a workgroup of 256 and of 1024 in the same way. Workgroups: about eight a CU of 256, a
+// worth, then a workgroup of 256 and of 1024 in the same way. Workgroups: up to eight a CU of 256, a
 // whole number of rows' groups together (the lanes of a group stay on its channels), none without an
 // item.
-bool norm_plan(int dtype, int64_t R, int G, int C, int shared, NormPlan* p) {
+bool norm_plan(int dtype, int64_t R, int G, int C, int shared, bool bwd, NormPlan* p) {
   p->vec = dtype == KDA_F32 ? 4 : 8;
   const int chunks = (C + p->vec - 1) / p->vec;
   p->tpi = 1;
@@ -370,8 +371,13 @@ bool norm_plan(int dtype, int64_t R, int G, int C, int shared, NormPlan* p) {
     h = r;
   }
   const int64_t step = G / g;
-  const int64_t full = p->tpi == 1024 ? 512 : 2048;
   const int64_t most = (R * G + subs - 1) / subs;
+  int64_t full = p->tpi == 1024 ? 512 : 2048;
+  if (bwd) {
+    // each workgroup leaves a row of sums: at least four items a group of lanes, but for a small call
+    full /= 2;
+    if (most / 4 < full) full = most / 4 > 256 ? most / 4 : 256;
+  }
   int64_t blocks = (full + step - 1) / step * step;
   if (blocks > most) blocks = (most + step - 1) / step * step;
   p->blocks = blocks;
@@ -383,7 +389,7 @@ bool norm_plan(int dtype, int64_t R, int G, int C, int shared, NormPlan* p) {
 hipError_t launch_norm_fwd(int dtype, const NormArgs& a, hipStream_t st) {
   if (a.R == 0) return hipSuccess;
   NormPlan p;
-  norm_plan(dtype, a.R, a.G, a.C, a.shared, &p);
+  norm_plan(dtype, a.R, a.G, a.C, a.shared, false, &p);
   NORM_DISPATCH(norm_fwd_t);
 }
 
@@ -395,22 +401,14 @@ hipError_t norm_bwd_main(int dtype, const NormArgs& a, const NormPlan& p, hipStr
 
 hipError_t launch_norm_bwd(int dtype, const NormArgs& a, hipStream_t st) {
   NormPlan p;
-  norm_plan(dtype, a.R, a.G, a.C, a.shared, &p);
+  norm_plan(dtype, a.R, a.G, a.C, a.shared, true, &p);
   if (a.R > 0) {
     const hipError_t e = norm_bwd_main(dtype, a, p, st);
     if (e != hipSuccess) return e;
   }
-  const int64_t rows = a.R > 0 ? p.part_rows : 0;
-  if (a.dw != nullptr) {
-    const hipError_t e = launch_col_sum(a.part, rows, p.part_cols, 2 * (int64_t)p.part_cols, a.dw, st);
-    if (e != hipSuccess) return e;
-  }
-  if (a.db != nullptr) return launch_col_sum(a.part + p.part_cols, rows, p.part_cols, 2 * (int64_t)p.part_cols, a.db, st);
-  return hipSuccess;
-}
-
-hipError_t launch_col_sum(const float* in, int64_t rows, int64_t cols, int64_t stride, float* out, hipStream_t st) {
-  hipLaunchKernelGGL(col_sum_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, st, in, rows, cols, stride, out);
+  if (a.dw == nullptr && a.db == nullptr) return hipSuccess;
+  hipLaunchKernelGGL(col_sum_kernel, dim3((unsigned)((2 * (int64_t)p.part_cols + 15) / 16)), dim3(1024), 0, st, a.part,
+                     a.R > 0 ? p.part_rows : 0, (int64_t)p.part_cols, a.dw, a.db);
   return hipGetLastError();
 }
 

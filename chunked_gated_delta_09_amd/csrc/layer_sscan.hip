@@ -824,48 +824,70 @@ __global__ __launch_bounds__(1024) void sscan_tables_kernel(const int32_t* cu, i
   if (threadIdx.x < 3) out[threadIdx.x][n] = base[threadIdx.x];
 }
 
-// One token: lanes as in the scan, the state read and written in place.
-template <class T, int NP>
+// One token: lanes as in the scan, the state read and written in place. A workgroup takes IT tiles of
+// channels, all loaded before the slot is checked.
+template <class T, int NP, int IT>
 __global__ __launch_bounds__(256) void sscan_step_kernel(ScanStepArgs a, int tiles) {
   typedef Lanes<NP> L;
   const int per = a.D / a.G;
-  const int grp = blockIdx.x / tiles, c0 = blockIdx.x % tiles * L::CH, b = blockIdx.y;
-  const int part = threadIdx.x % L::LPC, chl = threadIdx.x / L::LPC;
-  const int slot = step_slot(a.slots, b, a.slots_n);
-  const bool in = c0 + chl < per;
-  const int64_t d = (int64_t)grp * per + c0 + chl;
-  if (!in) return;
-  T* y = static_cast<T*>(a.y) + (int64_t)b * a.D + d;
-  if (slot < 0) {
-    if (part == 0) *y = (T)(slot == -1 ? 0.f : __builtin_nanf(""));
-    return;
+  const int grp = blockIdx.x / tiles, b = blockIdx.y;
+  const int part = threadIdx.x % L::LPC;
+  const int c0 = blockIdx.x % tiles * (L::CH * IT) + threadIdx.x / L::LPC;
+  const int asked = a.slots != nullptr ? a.slots[b] : b;
+  const bool held = asked >= 0 && asked < a.slots_n;
+  const int64_t d0 = (int64_t)grp * per + c0, row0 = (int64_t)(held ? asked : 0) * a.D + d0;
+  float h[IT][NPL], A[IT][NPL], x[IT], dt[IT], z[IT];
+#pragma unroll
+  for (int k = 0; k < IT; ++k) {
+    const bool in = c0 + k * L::CH < per;
+    const int64_t d = d0 + k * L::CH;
+    if (a.N == NP) {
+      unpack(in && held ? load_stream(a.state + (row0 + k * L::CH) * NP + part * NPL) : make_float4(0.f, 0.f, 0.f, 0.f), h[k]);
+    } else {
+      load_states<NP>(a.state, row0 + k * L::CH, a.N, part, in && held, h[k]);
+    }
+    load_states<NP>(a.A, d, a.N, part, in, A[k]);
+    x[k] = in ? as_f(static_cast<const T*>(a.x)[b * a.x_row + d]) : 0.f;
+    dt[k] = in ? as_f(static_cast<const T*>(a.dt)[b * a.dt_row + d]) + (a.dt_bias != nullptr ? a.dt_bias[d] : 0.f) : 0.f;
+    z[k] = in && a.z != nullptr ? as_f(static_cast<const T*>(a.z)[b * a.z_row + d]) : 0.f;
   }
-  float h[NPL], A[NPL];
-  const int64_t row = (int64_t)slot * a.D + d;
-  load_states<NP>(a.state, row, a.N, part, true, h);
-  load_states<NP>(a.A, d, a.N, part, true, A);
-  const float x = as_f(static_cast<const T*>(a.x)[b * a.x_row + d]);
-  float dt = as_f(static_cast<const T*>(a.dt)[b * a.dt_row + d]) + (a.dt_bias != nullptr ? a.dt_bias[d] : 0.f);
-  if (a.softplus) dt = softplus(dt);
+  float Bn[NPL], Cn[NPL];
   const T* Bm = static_cast<const T*>(a.Bm) + b * a.b_row + (int64_t)grp * a.N;
   const T* Cm = static_cast<const T*>(a.Cm) + b * a.c_row + (int64_t)grp * a.N;
-  float out = 0.f;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
     const int n = part * NPL + i;
-    const bool ok = n < a.N;
-    h[i] = fmaf(exp2_hw(dt * (A[i] * kLog2e)), h[i], dt * x * (ok ? as_f(Bm[n]) : 0.f));
-    out = fmaf(ok ? as_f(Cm[n]) : 0.f, h[i], out);
+    Bn[i] = n < a.N ? as_f(Bm[n]) : 0.f;
+    Cn[i] = n < a.N ? as_f(Cm[n]) : 0.f;
   }
-  store_states<NP>(a.state, row, a.N, part, true, h);
-  out = group_sum<L::LPC>(out);
-  if (part == 0) {
-    if (a.skip != nullptr) out = fmaf(a.skip[d], x, out);
-    if (a.z != nullptr) {
-      const float z = as_f(static_cast<const T*>(a.z)[b * a.z_row + d]);
-      out *= z * sigmoid(z);
+  const int slot = step_slot(a.slots, b, a.slots_n);
+#pragma unroll
+  for (int k = 0; k < IT; ++k) {
+    if (c0 + k * L::CH < per) {
+      const int64_t d = d0 + k * L::CH;
+      T* y = static_cast<T*>(a.y) + (int64_t)b * a.D + d;
+      if (slot < 0) {
+        if (part == 0) *y = (T)(slot == -1 ? 0.f : __builtin_nanf(""));
+      } else {
+        const float step = a.softplus ? softplus(dt[k]) : dt[k];
+        float out = 0.f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+          h[k][i] = fmaf(exp2_hw(step * (A[k][i] * kLog2e)), h[k][i], step * x[k] * Bn[i]);
+          out = fmaf(Cn[i], h[k][i], out);
+        }
+        if (a.N == NP)
+          store_stream(a.state + (row0 + k * L::CH) * NP + part * NPL, make_float4(h[k][0], h[k][1], h[k][2], h[k][3]));
+        else
+          store_states<NP>(a.state, row0 + k * L::CH, a.N, part, true, h[k]);
+        out = group_sum<L::LPC>(out);
+        if (part == 0) {
+          if (a.skip != nullptr) out = fmaf(a.skip[d], x[k], out);
+          if (a.z != nullptr) out *= z[k] * sigmoid(z[k]);
+          *y = (T)out;
+        }
+      }
     }
-    *y = (T)out;
   }
 }
 
@@ -907,10 +929,16 @@ hipError_t bwd_np(const ScanArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Four tiles of channels a workgroup where that still gives two workgroups a CU, one otherwise.
 template <class T, int NP>
 hipError_t step_np(const ScanStepArgs& a, hipStream_t st) {
-  const int tiles = scan_tiles(a.D, a.N, a.G);
-  hipLaunchKernelGGL((sscan_step_kernel<T, NP>), dim3(tiles * a.G, a.B), dim3(256), 0, st, a, tiles);
+  const int ch = Lanes<NP>::CH, per = a.D / a.G, wide = (per + 4 * ch - 1) / (4 * ch);
+  if ((int64_t)wide * a.G * a.B >= 512) {
+    hipLaunchKernelGGL((sscan_step_kernel<T, NP, 4>), dim3(wide * a.G, a.B), dim3(256), 0, st, a, wide);
+  } else {
+    const int tiles = (per + ch - 1) / ch;
+    hipLaunchKernelGGL((sscan_step_kernel<T, NP, 1>), dim3(tiles * a.G, a.B), dim3(256), 0, st, a, tiles);
+  }
   return hipGetLastError();
 }
 
