@@ -10,11 +10,6 @@ namespace kda {
 
 typedef __bf16 bf16;
 
-template <class T, int N>
-struct alignas(sizeof(T) * N) Vec {
-  T v[N];
-};
-
 __device__ __forceinline__ float as_f(bf16 x) { return (float)x; }
 __device__ __forceinline__ float as_f(float x) { return x; }
 
@@ -56,13 +51,26 @@ __device__ __forceinline__ Pack<T, N> load_n(const T* p, int valid, bool vec) {
   return r;
 }
 
+// N values to p, rounded to T; those from `valid` on are left. The 16-byte and the single stores take
+// different words, or the compiler joins the two ways into one of single stores.
 template <class T, int N>
 __device__ __forceinline__ void store_n(T* p, const float (&x)[N], int valid, bool vec) {
-  if (vec && valid >= N) {
-    Vec<T, N> r;
+  if (vec && valid >= N && N > 1) {
+    struct alignas(sizeof(T) * N < 4 ? 4 : sizeof(T) * N) Words {
+      uint32_t w[Pack<T, N>::WORDS];
+    } r;
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) r.v[i] = (T)x[i];
-    *reinterpret_cast<Vec<T, N>*>(p) = r;
+      for (int i = 0; i < N; ++i) r.w[i] = __float_as_uint(x[i]);
+    } else {
+      typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+      for (int i = 0; i + 1 < N; i += 2) {
+        const bf16x2 v = {(bf16)x[i], (bf16)x[i + 1]};
+        r.w[i / 2] = __builtin_bit_cast(uint32_t, v);
+      }
+    }
+    *reinterpret_cast<Words*>(p) = r;
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)

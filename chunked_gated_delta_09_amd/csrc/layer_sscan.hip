@@ -181,6 +181,29 @@ __device__ __forceinline__ void unpack(const float4& v, float (&out)[4]) {
   out[3] = v.w;
 }
 
+// dt of four channels from the raw steps; zero for a token that is not there, which leaves states as
+// they are.
+template <class T>
+__device__ __forceinline__ void steps_of(const Pack<T, 4>& raw, const float (&bias)[4], int soft, bool ok, float (&dt)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) dt[e] = raw.at(e) + bias[e];
+  if (soft) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dt[e] = softplus(dt[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) dt[e] = ok ? dt[e] : 0.f;
+}
+// v *= silu(z)
+template <class T>
+__device__ __forceinline__ void gate_by(const Pack<T, 4>& gate, float (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float z = gate.at(e);
+    v[e] *= z * sigmoid(z);
+  }
+}
+
 // The staging threads' sums of dt (16 a channel) to seg_dt of segment s; sh: [TT][CH].
 template <class T, int NP>
 __device__ __forceinline__ void sum_dt(const ScanArgs& a, const Stage<T, NP>& sv, const float (&total)[Lanes<NP>::ITEMS][4],
@@ -277,18 +300,15 @@ __global__ __launch_bounds__(256) void sscan_fwd_kernel(ScanArgs a, int tiles) {
       kx[k] = rx[k];
       kz[k] = rz[k];
       if (sv.has(k)) {
-        // a token behind the segment's end gets dt = 0: it leaves the state as it is
         const bool ok = sv.token(k) < live;
         float bias[4];
         unpack(*reinterpret_cast<const float4*>(&sBias[sv.col(k)]), bias);
         float2* to = &sX[sv.token(k)][sv.col(k)];
+        steps_of(rd[k], bias, a.softplus, ok, bias);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float dt = rd[k].at(e) + bias[e];
-          if (a.softplus) dt = softplus(dt);
-          dt = ok ? dt : 0.f;
-          if (!OUT) total[k][e] += dt;
-          to[e] = make_float2(dt, dt * rx[k].at(e));
+          if (!OUT) total[k][e] += bias[e];
+          to[e] = make_float2(bias[e], bias[e] * rx[k].at(e));
         }
       }
     }
@@ -326,13 +346,8 @@ __global__ __launch_bounds__(256) void sscan_fwd_kernel(ScanArgs a, int tiles) {
           unpack(*reinterpret_cast<const float4*>(&sSkip[sv.col(k)]), skip);
           unpack(*reinterpret_cast<const float4*>(&sY[sv.token(k)][sv.col(k)]), out);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            out[e] = fmaf(skip[e], kx[k].at(e), out[e]);
-            if (a.z != nullptr) {
-              const float z = kz[k].at(e);
-              out[e] *= z * sigmoid(z);
-            }
-          }
+          for (int e = 0; e < 4; ++e) out[e] = fmaf(skip[e], kx[k].at(e), out[e]);
+          if (a.z != nullptr) gate_by(kz[k], out);
           sv.store(a.y, sg.t0 + at, a.D, oy[k], k, live, out);
         }
     }
@@ -409,18 +424,15 @@ __global__ __launch_bounds__(256) void sscan_bwd_local_kernel(ScanArgs a, int ti
         float bias[4];
         unpack(*reinterpret_cast<const float4*>(&sBias[sv.col(k)]), bias);
         float2* to = &sX[sv.token(k)][sv.col(k)];
+        steps_of(rd[k], bias, a.softplus, ok, bias);
+        float g[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[e] = ry[k].at(e);
+        if (a.z != nullptr) gate_by(rz[k], g);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float dt = rd[k].at(e) + bias[e];
-          if (a.softplus) dt = softplus(dt);
-          dt = ok ? dt : 0.f;
-          total[k][e] += dt;
-          float g = ry[k].at(e);
-          if (a.z != nullptr) {
-            const float z = rz[k].at(e);
-            g *= z * sigmoid(z);
-          }
-          to[e] = make_float2(dt, g);
+          total[k][e] += bias[e];
+          to[e] = make_float2(bias[e], g[e]);
         }
       }
 #pragma unroll
@@ -565,18 +577,13 @@ __global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles
         float bias[4], g4[4];
         unpack(*reinterpret_cast<const float4*>(&sBias[sv.col(k)]), bias);
         float2* to = &sX[sv.token(k)][sv.col(k)];
+        steps_of(rd[k], bias, a.softplus, ok, bias);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float dt = rd[k].at(e) + bias[e];
-          if (a.softplus) dt = softplus(dt);
-          dt = ok ? dt : 0.f;
           g4[e] = ry[k].at(e);
-          if (GATE) {
-            const float z = rz[k].at(e);
-            g4[e] *= z * sigmoid(z);
-          }
-          to[e] = make_float2(dt, dt * rx[k].at(e));
+          to[e] = make_float2(bias[e], bias[e] * rx[k].at(e));
         }
+        if (GATE) gate_by(rz[k], g4);
         *reinterpret_cast<float4*>(&sG[sv.token(k)][sv.col(k)]) = make_float4(g4[0], g4[1], g4[2], g4[3]);
       }
     }
@@ -710,10 +717,14 @@ __global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles
           }
           vx[e] = fmaf(sX[pt][pc + e].x, s1[e], skip[e] * g);
           vd[e] = fmaf(x, s1[e], s2[e]);
-          if (a.softplus) vd[e] *= sigmoid(kd[k].at(e) + bias[e]);
           dskip[k][e] = fmaf(g, x, dskip[k][e]);
-          dbias[k][e] += ok ? vd[e] : 0.f;
         }
+        if (a.softplus) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) vd[e] *= sigmoid(kd[k].at(e) + bias[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dbias[k][e] += ok ? vd[e] : 0.f;
         sv.store(a.dx, sg.t0 + at, a.D, oy[k], k, live, vx);
         sv.store(a.ddt, sg.t0 + at, a.D, oy[k], k, live, vd);
         if (a.dz != nullptr) sv.store(a.dz, sg.t0 + at, a.D, oy[k], k, live, vz);
