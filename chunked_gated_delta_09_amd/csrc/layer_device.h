@@ -99,14 +99,14 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 // 1 / (1 + e^-x): e^-x overflows to infinity for x < -88.7, where the quotient is zero as it should be.
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + exp2_hw(-kLog2e * x)); }
 // log(1 + e^x) = max(x, 0) + log1p(e^-|x|): no overflow, and full relative precision for very
-// negative x, where it is e^x. log1p(e) with u = 1 + e rounded is log(u) + (e - (u - 1)) / u.
-// `slope`: its derivative, 1 / (1 + e^-x).
-__device__ __forceinline__ float softplus(float x, float* slope = nullptr) {
+// negative x, where it is e^x. With u = 1 + e rounded, log1p(e) is log(u) + (e - (u - 1)) / u; u is in
+// [1, 2], so the hardware's log2 needs none of a general logarithm's scaling.
+__device__ __forceinline__ float softplus(float x) {
   const float e = exp2_hw(-kLog2e * fabsf(x));
-  const float u = 1.f + e, v = __builtin_amdgcn_rcpf(u);
-  if (slope != nullptr) *slope = x >= 0.f ? v : e * v;
-  // the median with 0 and infinity is max(x, 0) in one instruction
-  return __builtin_amdgcn_fmed3f(x, 0.f, __builtin_inff()) + (__logf(u) + (e - (u - 1.f)) * v);
+  const float u = 1.f + e;
+  float top;  // one instruction; fmaxf is two, the first for signalling NaN
+  asm("v_max_f32 %0, 0, %1" : "=v"(top) : "v"(x));
+  return fmaf(__builtin_amdgcn_logf(u), 0.6931471805599453f, fmaf(e - (u - 1.f), __builtin_amdgcn_rcpf(u), top));
 }
 
 // y = act(x) and its derivative for kda_act codes.
