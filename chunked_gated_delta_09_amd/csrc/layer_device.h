@@ -92,7 +92,7 @@ __device__ __forceinline__ void store_stream(float* p, float4 v) {
   __builtin_nontemporal_store(w, reinterpret_cast<f4*>(p));
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // 2^x by the hardware instruction (results below the normal range become zero).
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -106,7 +106,7 @@ __device__ __forceinline__ float softplus(float x) {
   const float u = 1.f + e;
   float top;  // one instruction; fmaxf is two, the first for signalling NaN
   asm("v_max_f32 %0, 0, %1" : "=v"(top) : "v"(x));
-  return fmaf(__builtin_amdgcn_logf(u), 0.6931471805599453f, fmaf(e - (u - 1.f), __builtin_amdgcn_rcpf(u), top));
+  return fmaf(__builtin_amdgcn_logf(u), kLn2, fmaf(e - (u - 1.f), __builtin_amdgcn_rcpf(u), top));
 }
 
 // y = act(x) and its derivative for kda_act codes.

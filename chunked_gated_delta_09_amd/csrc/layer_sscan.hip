@@ -504,11 +504,11 @@ __global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles
   const int tid = threadIdx.x, part = tid % L::LPC, chl = tid / L::LPC, lane = tid % 64, wave = tid / 64;
   const bool in = c0 + chl < sv.per;
   const int64_t d = (int64_t)grp * sv.per + c0 + chl;
-  float A[NPL], A2[NPL], q[NPL], dA[NPL];
-  load_states<NP>(a.A, d, a.N, part, in, A);
+  float A2[NPL], q[NPL], dA[NPL];
+  load_states<NP>(a.A, d, a.N, part, in, A2);
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
-    A2[i] = A[i] * kLog2e;
+    A2[i] *= kLog2e;
     q[i] = dA[i] = 0.f;
   }
   if (a.dfinal != nullptr) load_states<NP>(a.dfinal, (int64_t)sg.n * a.D + d, a.N, part, in, q);
@@ -666,7 +666,7 @@ __global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles
           s1 = fmaf(r, bb[i], s1);
           q[i] = as[u][i] * r;
           const float p = q[i] * hs[u][i];
-          s2 = fmaf(p, A[i], s2);
+          s2 = fmaf(p, A2[i], s2);
           dAc[i] = fmaf(p, v.x, dAc[i]);
         }
         s1 = group_sum<L::LPC>(s1);
@@ -716,7 +716,7 @@ __global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles
             g *= z * s;
           }
           vx[e] = fmaf(sX[pt][pc + e].x, s1[e], skip[e] * g);
-          vd[e] = fmaf(x, s1[e], s2[e]);
+          vd[e] = fmaf(x, s1[e], s2[e] * kLn2);  // A2 holds A log2 e
           dskip[k][e] = fmaf(g, x, dskip[k][e]);
         }
         if (a.softplus) {
@@ -735,7 +735,8 @@ __global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles
         a.part_bc[(((int64_t)tile * a.sq.total + sg.t0 + at + pt) * a.G + grp) * 2 * NP + v] =
             (sS[0][pt][v] + sS[1][pt][v]) + (sS[2][pt][v] + sS[3][pt][v]);
     }
-    __syncthreads();
+    // no barrier: the next chunk's staging overwrites sX and sG only at the places that this thread itself
+    // has just read, and sB and sC, which were last read before the barrier above
   }
   const int64_t s = sg.first + sg.j;
   if (a.dh0 != nullptr && sg.j == 0) store_states<NP>(a.dh0, (int64_t)sg.n * a.D + d, a.N, part, in, q);
