@@ -18,8 +18,8 @@ on the GPU: no state is touched for that row and its output is NaN.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -82,52 +82,47 @@ def _lib():
     return _ready
 
 
-def _on(dev):
-    """The library launches on the current device: make it the tensors' for the call."""
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+def _launch(dev, fn, *args):
+    """Calls fn(*args, stream) with GPU `dev` and its current stream. Kernels go to the current device."""
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _check(status)
 
 
-def _stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
-
-
-def _p(t):
-    return None if t is None else t.data_ptr()
-
-
-def _need(t, name, dtype, shape, dev):
-    """A contiguous tensor of this type and shape on `dev` (None passes)."""
-    if t is None:
-        return
+def _refuse(t, name, dtype, shape, dev):
+    """Raises for what is wrong with `t`, layout apart."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on GPU {dev} like the others, got {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+
+
+def _need(t, name, dtype, shape, dev):
+    """The address of a contiguous tensor of this type and shape on GPU `dev` (None passes)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, dev)
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows(t, name, dtype, shape, dev, lead):
     """As _need for a tensor that may be a column slice: the first `lead` dimensions are its rows.
-    Returns the elements between two rows."""
+    Returns the address and the elements between two rows (0: contiguous)."""
     if t is None:
-        return 0
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.is_contiguous():
-        return 0
+        return None, 0
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr(), 0
+    _refuse(t, name, dtype, shape, dev)
     width, row = 1, None
     for i in range(t.dim() - 1, lead - 1, -1):
         if t.shape[i] != 1 and t.stride(i) != width:
@@ -143,15 +138,16 @@ def _rows(t, name, dtype, shape, dev, lead):
             elif t.stride(i) != row * count:
                 raise ValueError(f"{name} must be contiguous or a column slice of a contiguous tensor")
         count *= t.shape[i]
-    return row or 0
+    return t.data_ptr(), row or 0
 
 
 def _gpu(t, name):
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype not in _DT:
         raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
-    return t.device
+    return dev
 
 
 def _act(activation, allowed):
@@ -161,20 +157,40 @@ def _act(activation, allowed):
 
 
 def _cuts(cu_seqlens, cu_seqlens_dev, B, dev):
-    """(sequences, device cuts or None, host array or None)."""
+    """(sequences, address of the device cuts or None, host array or None, what must live until the call)."""
     if cu_seqlens is None:
         if cu_seqlens_dev is not None:
             raise ValueError("cu_seqlens_dev needs the host list cu_seqlens beside it")
-        return B, None, None
+        return B, None, None, None
     if B != 1:
         raise ValueError("packed sequences need batch size 1")
     cu = [int(c) for c in (cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens)]
     if len(cu) < 2:
         raise ValueError("cu_seqlens needs at least two entries")
     if cu_seqlens_dev is None:
-        cu_seqlens_dev = torch.tensor(cu, dtype=torch.int32, device=dev)
-    _need(cu_seqlens_dev, "cu_seqlens_dev", torch.int32, (len(cu),), dev)
-    return len(cu) - 1, cu_seqlens_dev, (_i32 * len(cu))(*cu)
+        cu_seqlens_dev = torch.tensor(cu, dtype=torch.int32, device=f"cuda:{dev}")
+    ptr = _need(cu_seqlens_dev, "cu_seqlens_dev", torch.int32, (len(cu),), dev)
+    return len(cu) - 1, ptr, (_i32 * len(cu))(*cu), cu_seqlens_dev
+
+
+# The size structures of calls without cuts, by their values: the library only reads them.
+@functools.lru_cache(maxsize=512)
+def _dims(kind, *values):
+    d = kind(*values)
+    return d, ctypes.byref(d)
+
+
+def _dims_of(kind, cu_dev, cu_host, before, after):
+    if cu_host is None:
+        return _dims(kind, *before, None, None, *after)
+    d = kind(*before, cu_dev, cu_host, *after)
+    return d, ctypes.byref(d)
+
+
+@functools.lru_cache(maxsize=512)
+def _kda_dims(B, H, HV, K, V, scale, dtype, beta_logits):
+    d, _ = make_dims(B, 1, H, HV, K, V, 16, scale, dtype, beta_logits=beta_logits)
+    return d, ctypes.byref(d)
 
 
 def _bytes(n):
@@ -183,12 +199,24 @@ def _bytes(n):
     return n
 
 
-def _ws(n, dev):
-    return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+def _ws(like, n):
+    """A workspace of n bytes and its address."""
+    if not n:
+        return None, None
+    ws = torch.empty(n, dtype=torch.uint8, device=like.device)
+    return ws, ws.data_ptr()
 
 
-def _slots(slots, B, dev):
-    _need(slots, "slots", torch.int32, (B,), dev)
+def _new(like, shape, dtype=None):
+    t = like.new_empty(shape, dtype=dtype)
+    return t, t.data_ptr()
+
+
+def _new_if(cond, like, shape, dtype=None):
+    return _new(like, shape, dtype) if cond else (None, None)
+
+
+F32 = torch.float32
 
 
 # ---- short convolution
@@ -200,13 +228,12 @@ def _conv(x, weight, bias, h0, cu_seqlens, cu_seqlens_dev, activation):
         raise ValueError("x must be [B, T, D] and weight [D, W]")
     B, T, D = x.shape
     W = weight.shape[1]
-    N, cu_dev, cu_host = _cuts(cu_seqlens, cu_seqlens_dev, B, dev)
-    row = _rows(x, "x", x.dtype, (B, T, D), dev, 2)
-    _need(weight, "weight", torch.float32, (D, W), dev)
-    _need(bias, "bias", torch.float32, (D,), dev)
-    _need(h0, "h0", x.dtype, (N, W - 1, D), dev)
-    d = _ConvDims(B, T, D, W, N, _p(cu_dev), cu_host, row, _act(activation, (None, "silu")), _DT[x.dtype])
-    return d, dev, (B, T, D, W, N), (cu_dev, cu_host)
+    N, cu_dev, cu_host, keep = _cuts(cu_seqlens, cu_seqlens_dev, B, dev)
+    px, row = _rows(x, "x", x.dtype, (B, T, D), dev, 2)
+    ptrs = (px, _need(weight, "weight", F32, (D, W), dev), _need(bias, "bias", F32, (D,), dev),
+            _need(h0, "h0", x.dtype, (N, W - 1, D), dev))
+    d = _dims_of(_ConvDims, cu_dev, cu_host, (B, T, D, W, N), (row, _act(activation, (None, "silu")), _DT[x.dtype]))
+    return d[1], dev, (B, T, D, W, N), ptrs, (d, keep)
 
 
 def short_conv(x, weight, bias=None, h0=None, cu_seqlens=None, cu_seqlens_dev=None, activation="silu",
@@ -215,12 +242,10 @@ def short_conv(x, weight, bias=None, h0=None, cu_seqlens=None, cu_seqlens_dev=No
     x_{t-(W-1)+j}, y = u or silu(u). x [B,T,D]; weight [D,W] fp32 (W = 2, 3, 4; the last tap sees the
     current token); bias [D] fp32; h0 [N,W-1,D]: the rows before each sequence's first. Returns
     dict(y [B,T,D], final_state [N,W-1,D] or None: the last W-1 rows of [h0 | x])."""
-    d, dev, (B, T, D, W, N), keep = _conv(x, weight, bias, h0, cu_seqlens, cu_seqlens_dev, activation)
-    with _on(dev):
-        y = torch.empty(B, T, D, dtype=x.dtype, device=dev)
-        final = torch.empty(N, W - 1, D, dtype=x.dtype, device=dev) if output_final_state else None
-        _check(_lib().kda_short_conv_fwd(ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(h0), _p(y), _p(final),
-                                         _stream(dev)))
+    d, dev, (B, T, D, W, N), ptrs, keep = _conv(x, weight, bias, h0, cu_seqlens, cu_seqlens_dev, activation)
+    y, py = _new(x, (B, T, D))
+    final, pf = _new_if(output_final_state, x, (N, W - 1, D))
+    _launch(dev, _lib().kda_short_conv_fwd, d, *ptrs, py, pf)
     del keep
     return dict(y=y, final_state=final)
 
@@ -229,19 +254,17 @@ def short_conv_bwd(x, weight, dy, bias=None, h0=None, dfinal=None, cu_seqlens=No
                    activation="silu"):
     """Gradients of sum<dy, y> + <dfinal, final_state>. Returns dict(dx [B,T,D], dweight [D,W] fp32,
     dbias [D] fp32 or None, dh0 [N,W-1,D] or None)."""
-    d, dev, (B, T, D, W, N), keep = _conv(x, weight, bias, h0, cu_seqlens, cu_seqlens_dev, activation)
-    _need(dy, "dy", x.dtype, (B, T, D), dev)
-    _need(dfinal, "dfinal", x.dtype, (N, W - 1, D), dev)
+    d, dev, (B, T, D, W, N), ptrs, keep = _conv(x, weight, bias, h0, cu_seqlens, cu_seqlens_dev, activation)
+    pdy = _need(dy, "dy", x.dtype, (B, T, D), dev)
+    pdf = _need(dfinal, "dfinal", x.dtype, (N, W - 1, D), dev)
     lib = _lib()
-    need = lib.kda_short_conv_bwd_workspace_bytes(ctypes.byref(d))
-    with _on(dev):
-        dx = torch.empty(B, T, D, dtype=x.dtype, device=dev)
-        dw = torch.empty_like(weight)
-        db = torch.empty_like(bias) if bias is not None else None
-        dh0 = torch.empty_like(h0) if h0 is not None else None
-        ws = _ws(need, dev)
-        _check(lib.kda_short_conv_bwd(ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(h0), _p(dy), _p(dfinal), _p(dx),
-                                      _p(dw), _p(db), _p(dh0), _p(ws), need, _stream(dev)))
+    need = lib.kda_short_conv_bwd_workspace_bytes(d)
+    dx, pdx = _new(x, (B, T, D))
+    dw, pdw = _new(x, (D, W), F32)
+    db, pdb = _new_if(bias is not None, x, (D,), F32)
+    dh0, pdh0 = _new_if(h0 is not None, x, (N, W - 1, D))
+    ws, pws = _ws(x, need)
+    _launch(dev, lib.kda_short_conv_bwd, d, *ptrs, pdy, pdf, pdx, pdw, pdb, pdh0, pws, need)
     del keep
     return dict(dx=dx, dweight=dw, dbias=db, dh0=dh0)
 
@@ -252,18 +275,15 @@ def short_conv_step(x, state, weight, bias=None, slots=None, activation="silu"):
     dev = _gpu(x, "x")
     if x.dim() != 2 or weight.dim() != 2 or state.dim() != 3:
         raise ValueError("x must be [B, D], weight [D, W] and state [S, W-1, D]")
-    B, D = x.shape
-    W = weight.shape[1]
-    row = _rows(x, "x", x.dtype, (B, D), dev, 1)
-    _need(weight, "weight", torch.float32, (D, W), dev)
-    _need(bias, "bias", torch.float32, (D,), dev)
-    _need(state, "state", x.dtype, (state.shape[0], W - 1, D), dev)
-    _slots(slots, B, dev)
-    d = _ConvDims(B, 1, D, W, B, None, None, row, _act(activation, (None, "silu")), _DT[x.dtype])
-    with _on(dev):
-        y = torch.empty(B, D, dtype=x.dtype, device=dev)
-        _check(_lib().kda_short_conv_step(ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(slots), state.shape[0],
-                                          _p(state), _p(y), _stream(dev)))
+    (B, D), S, W = x.shape, state.shape[0], weight.shape[1]
+    px, row = _rows(x, "x", x.dtype, (B, D), dev, 1)
+    pw = _need(weight, "weight", F32, (D, W), dev)
+    pb = _need(bias, "bias", F32, (D,), dev)
+    pst = _need(state, "state", x.dtype, (S, W - 1, D), dev)
+    psl = _need(slots, "slots", torch.int32, (B,), dev)
+    _, d = _dims(_ConvDims, B, 1, D, W, B, None, None, row, _act(activation, (None, "silu")), _DT[x.dtype])
+    y, py = _new(x, (B, D))
+    _launch(dev, _lib().kda_short_conv_step, d, px, pw, pb, psl, S, pst, py)
     return y
 
 
@@ -275,18 +295,20 @@ def _scan(x, dt, A, B, C, skip, z, dt_bias, softplus, lead, cuts):
     if x.dim() != lead + 1 or A.dim() != 2 or B.dim() != lead + 2:
         raise ValueError("x must be %s, A [D, NS] and B, C %s" % (("[B, T, D]", "[B, T, G, NS]") if lead == 2 else
                                                                    ("[B, D]", "[B, G, NS]")))
-    rows, D, NS, G = tuple(x.shape[:-1]), x.shape[-1], A.shape[1], B.shape[-2]
-    N, cu_dev, cu_host = _cuts(*cuts, rows[0], dev)
-    dt_ = x.dtype
-    strides = [_rows(x, "x", dt_, rows + (D,), dev, lead), _rows(dt, "dt", dt_, rows + (D,), dev, lead),
-               _rows(z, "z", dt_, rows + (D,), dev, lead), _rows(B, "B", dt_, rows + (G, NS), dev, lead),
-               _rows(C, "C", dt_, rows + (G, NS), dev, lead)]
-    _need(A, "A", torch.float32, (D, NS), dev)
-    _need(skip, "skip", torch.float32, (D,), dev)
-    _need(dt_bias, "dt_bias", torch.float32, (D,), dev)
-    d = _ScanDims(rows[0], rows[1] if lead == 2 else 1, D, NS, G, N, _p(cu_dev), cu_host, *strides, int(bool(softplus)),
-                  _DT[dt_])
-    return d, dev, (rows, D, NS, G, N), (cu_dev, cu_host)
+    shape, D, NS, G, dt_ = x.shape, x.shape[-1], A.shape[1], B.shape[-2], x.dtype
+    rows = tuple(shape[:-1])
+    bc = rows + (G, NS)
+    N, cu_dev, cu_host, keep = _cuts(*cuts, rows[0], dev)
+    px, rx = _rows(x, "x", dt_, shape, dev, lead)
+    pdt, rdt = _rows(dt, "dt", dt_, shape, dev, lead)
+    pz, rz = _rows(z, "z", dt_, shape, dev, lead)
+    pB, rB = _rows(B, "B", dt_, bc, dev, lead)
+    pC, rC = _rows(C, "C", dt_, bc, dev, lead)
+    ptrs = (px, pdt, _need(A, "A", F32, (D, NS), dev), pB, pC, _need(skip, "skip", F32, (D,), dev), pz,
+            _need(dt_bias, "dt_bias", F32, (D,), dev))
+    d = _dims_of(_ScanDims, cu_dev, cu_host, (rows[0], rows[1] if lead == 2 else 1, D, NS, G, N),
+                 (rx, rdt, rz, rB, rC, int(bool(softplus)), _DT[dt_]))
+    return d[1], dev, (rows, D, NS, G, N), ptrs, (d, keep)
 
 
 def selective_scan(x, dt, A, B, C, skip=None, z=None, dt_bias=None, h0=None, cu_seqlens=None, cu_seqlens_dev=None,
@@ -296,21 +318,19 @@ def selective_scan(x, dt, A, B, C, skip=None, z=None, dt_bias=None, h0=None, cu_
     [B,T,G,NS], shared by the D/G channels of a group; skip, dt_bias [D] fp32; h0 [N,D,NS] fp32.
     Returns dict(y [B,T,D], final_state [N,D,NS] fp32 or None, states or None). ``save``: keep the state
     entering every SCAN_CHUNK tokens (fp32 [chunks,D,NS]) for ``selective_scan_bwd``."""
-    d, dev, (rows, D, NS, G, N), keep = _scan(x, dt, A, B, C, skip, z, dt_bias, dt_softplus, 2,
-                                              (cu_seqlens, cu_seqlens_dev))
-    _need(h0, "h0", torch.float32, (N, D, NS), dev)
+    d, dev, (rows, D, NS, G, N), ptrs, keep = _scan(x, dt, A, B, C, skip, z, dt_bias, dt_softplus, 2,
+                                                    (cu_seqlens, cu_seqlens_dev))
+    ph0 = _need(h0, "h0", F32, (N, D, NS), dev)
     lib = _lib()
-    chunks = lib.kda_sscan_num_chunks(ctypes.byref(d))
+    chunks = lib.kda_sscan_num_chunks(d)
     if chunks < 0:
         raise KdaError(-1, lib.kda_last_error().decode())
-    need = lib.kda_sscan_fwd_workspace_bytes(ctypes.byref(d))
-    with _on(dev):
-        y = torch.empty(*rows, D, dtype=x.dtype, device=dev)
-        final = torch.empty(N, D, NS, dtype=torch.float32, device=dev) if output_final_state else None
-        states = torch.empty(chunks, D, NS, dtype=torch.float32, device=dev) if save else None
-        ws = _ws(need, dev)
-        _check(lib.kda_sscan_fwd(ctypes.byref(d), _p(x), _p(dt), _p(A), _p(B), _p(C), _p(skip), _p(z), _p(dt_bias),
-                                 _p(h0), _p(y), _p(final), _p(states), _p(ws), need, _stream(dev)))
+    need = lib.kda_sscan_fwd_workspace_bytes(d)
+    y, py = _new(x, rows + (D,))
+    final, pf = _new_if(output_final_state, x, (N, D, NS), F32)
+    states, ps = _new_if(save, x, (chunks, D, NS), F32)
+    ws, pws = _ws(x, need)
+    _launch(dev, lib.kda_sscan_fwd, d, *ptrs, ph0, py, pf, ps, pws, need)
     del keep
     return dict(y=y, final_state=final, states=states)
 
@@ -321,30 +341,25 @@ def selective_scan_bwd(x, dt, A, B, C, states, dy, skip=None, z=None, dt_bias=No
     ``selective_scan(..., save=True)`` on the same arguments. Returns dict(dx, ddt [B,T,D], dA [D,NS]
     fp32, dB, dC [B,T,G,NS], dskip [D] fp32 or None, dz [B,T,D] or None, ddt_bias [D] fp32 or None, dh0
     [N,D,NS] fp32 or None)."""
-    d, dev, (rows, D, NS, G, N), keep = _scan(x, dt, A, B, C, skip, z, dt_bias, dt_softplus, 2,
-                                              (cu_seqlens, cu_seqlens_dev))
+    d, dev, (rows, D, NS, G, N), ptrs, keep = _scan(x, dt, A, B, C, skip, z, dt_bias, dt_softplus, 2,
+                                                    (cu_seqlens, cu_seqlens_dev))
     lib = _lib()
-    chunks = lib.kda_sscan_num_chunks(ctypes.byref(d))
+    chunks = lib.kda_sscan_num_chunks(d)
     if chunks < 0:
         raise KdaError(-1, lib.kda_last_error().decode())
-    _need(states, "states", torch.float32, (chunks, D, NS), dev)
-    _need(dy, "dy", x.dtype, rows + (D,), dev)
-    _need(dfinal, "dfinal", torch.float32, (N, D, NS), dev)
-    need = _bytes(lib.kda_sscan_bwd_workspace_bytes(ctypes.byref(d)))
-    f32 = dict(dtype=torch.float32, device=dev)
-    own = dict(dtype=x.dtype, device=dev)
-    with _on(dev):
-        dx, ddt = torch.empty(*rows, D, **own), torch.empty(*rows, D, **own)
-        dA = torch.empty(D, NS, **f32)
-        dB, dC = torch.empty(*rows, G, NS, **own), torch.empty(*rows, G, NS, **own)
-        dskip = torch.empty(D, **f32) if skip is not None else None
-        dz = torch.empty(*rows, D, **own) if z is not None else None
-        dbias = torch.empty(D, **f32) if dt_bias is not None else None
-        dh0 = torch.empty(N, D, NS, **f32) if output_dh0 else None
-        ws = _ws(need, dev)
-        _check(lib.kda_sscan_bwd(ctypes.byref(d), _p(x), _p(dt), _p(A), _p(B), _p(C), _p(skip), _p(z), _p(dt_bias),
-                                 _p(states), _p(dy), _p(dfinal), _p(dx), _p(ddt), _p(dA), _p(dB), _p(dC), _p(dskip),
-                                 _p(dz), _p(dbias), _p(dh0), _p(ws), need, _stream(dev)))
+    pst = _need(states, "states", F32, (chunks, D, NS), dev)
+    pdy = _need(dy, "dy", x.dtype, rows + (D,), dev)
+    pdf = _need(dfinal, "dfinal", F32, (N, D, NS), dev)
+    need = _bytes(lib.kda_sscan_bwd_workspace_bytes(d))
+    wide, bc = rows + (D,), rows + (G, NS)
+    (dx, pdx), (ddt, pddt), (dA, pdA) = _new(x, wide), _new(x, wide), _new(x, (D, NS), F32)
+    (dB, pdB), (dC, pdC) = _new(x, bc), _new(x, bc)
+    dskip, pds = _new_if(skip is not None, x, (D,), F32)
+    dz, pdz = _new_if(z is not None, x, wide)
+    dbias, pdb = _new_if(dt_bias is not None, x, (D,), F32)
+    dh0, pdh0 = _new_if(output_dh0, x, (N, D, NS), F32)
+    ws, pws = _ws(x, need)
+    _launch(dev, lib.kda_sscan_bwd, d, *ptrs, pst, pdy, pdf, pdx, pddt, pdA, pdB, pdC, pds, pdz, pdb, pdh0, pws, need)
     del keep
     return dict(dx=dx, ddt=ddt, dA=dA, dB=dB, dC=dC, dskip=dskip, dz=dz, ddt_bias=dbias, dh0=dh0)
 
@@ -352,15 +367,15 @@ def selective_scan_bwd(x, dt, A, B, C, states, dy, skip=None, z=None, dt_bias=No
 def selective_scan_step(x, dt, A, B, C, state, slots=None, skip=None, z=None, dt_bias=None, dt_softplus=False):
     """One token of each sequence: x, dt, z [B,D], B, C [B,G,NS], state [S,D,NS] fp32 updated in place.
     Returns y [B,D]."""
-    d, dev, (rows, D, NS, G, N), _ = _scan(x, dt, A, B, C, skip, z, dt_bias, dt_softplus, 1, (None, None))
+    d, dev, (rows, D, NS, G, N), ptrs, keep = _scan(x, dt, A, B, C, skip, z, dt_bias, dt_softplus, 1, (None, None))
     if state.dim() != 3:
         raise ValueError("state must be [S, D, NS]")
-    _need(state, "state", torch.float32, (state.shape[0], D, NS), dev)
-    _slots(slots, rows[0], dev)
-    with _on(dev):
-        y = torch.empty(rows[0], D, dtype=x.dtype, device=dev)
-        _check(_lib().kda_sscan_step(ctypes.byref(d), _p(x), _p(dt), _p(A), _p(B), _p(C), _p(skip), _p(z), _p(dt_bias),
-                                     _p(slots), state.shape[0], _p(state), _p(y), _stream(dev)))
+    S = state.shape[0]
+    pst = _need(state, "state", F32, (S, D, NS), dev)
+    psl = _need(slots, "slots", torch.int32, rows, dev)
+    y, py = _new(x, rows + (D,))
+    _launch(dev, _lib().kda_sscan_step, d, *ptrs, psl, S, pst, py)
+    del keep
     return y
 
 
@@ -369,20 +384,20 @@ def selective_scan_step(x, dt, A, B, C, state, slots=None, skip=None, z=None, dt
 
 def _norm(x, groups, weight, bias, gate, activation, center, eps):
     dev = _gpu(x, "x")
-    if x.dim() < 1 or groups < 1 or x.shape[-1] == 0 or x.shape[-1] % groups:
-        raise ValueError(f"the last dimension of x must be a positive multiple of groups ({groups}), got {tuple(x.shape)}")
-    lead = x.dim() - 1
-    W = x.shape[-1]
+    shape = x.shape
+    if not shape or groups < 1 or shape[-1] == 0 or shape[-1] % groups:
+        raise ValueError(f"the last dimension of x must be a positive multiple of groups ({groups}), got {tuple(shape)}")
+    lead, W = len(shape) - 1, shape[-1]
     C = W // groups
-    x_row = _rows(x, "x", x.dtype, x.shape, dev, lead)
-    gate_row = _rows(gate, "gate", x.dtype, x.shape, dev, lead)
+    px, x_row = _rows(x, "x", x.dtype, shape, dev, lead)
+    pg, gate_row = _rows(gate, "gate", x.dtype, shape, dev, lead)
     first = weight if weight is not None else bias
     shared = first is not None and groups > 1 and first.dim() == 1 and first.shape[0] == C
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        _need(t, name, torch.float32, (C if shared else W,), dev)
-    d = _NormDims(x.numel() // W, groups, C, int(bool(center)), _act(activation, (None, "silu", "sigmoid")), int(shared),
-                  float(eps), x_row, gate_row, _DT[x.dtype])
-    return d, dev
+    n = (C if shared else W,)
+    ptrs = (px, _need(weight, "weight", F32, n, dev), _need(bias, "bias", F32, n, dev), pg)
+    _, d = _dims(_NormDims, x.numel() // W, groups, C, int(bool(center)), _act(activation, (None, "silu", "sigmoid")),
+                 int(shared), float(eps), x_row, gate_row, _DT[x.dtype])
+    return d, dev, ptrs
 
 
 def group_norm(x, groups, weight=None, bias=None, gate=None, activation=None, center=False, eps=1e-5):
@@ -390,27 +405,24 @@ def group_norm(x, groups, weight=None, bias=None, gate=None, activation=None, ce
     ``center``, (x - mean) / std), u = n weight + bias, y = act(u), or u act(gate) with a gate of x's
     shape. weight and bias fp32, [groups*C] or [C] (one for all groups). activation: None, "silu",
     "sigmoid". Returns y."""
-    d, dev = _norm(x, groups, weight, bias, gate, activation, center, eps)
-    with _on(dev):
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        _check(_lib().kda_group_norm_fwd(ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(gate), _p(y), _stream(dev)))
+    d, dev, ptrs = _norm(x, groups, weight, bias, gate, activation, center, eps)
+    y, py = _new(x, x.shape)
+    _launch(dev, _lib().kda_group_norm_fwd, d, *ptrs, py)
     return y
 
 
 def group_norm_bwd(x, groups, dy, weight=None, bias=None, gate=None, activation=None, center=False, eps=1e-5):
     """Gradients of sum<dy, y>. Returns dict(dx, dweight, dbias, dgate), None where the input is."""
-    d, dev = _norm(x, groups, weight, bias, gate, activation, center, eps)
-    _need(dy, "dy", x.dtype, x.shape, dev)
+    d, dev, ptrs = _norm(x, groups, weight, bias, gate, activation, center, eps)
+    pdy = _need(dy, "dy", x.dtype, x.shape, dev)
     lib = _lib()
-    need = lib.kda_group_norm_bwd_workspace_bytes(ctypes.byref(d)) if weight is not None or bias is not None else 0
-    with _on(dev):
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        dw = torch.empty_like(weight) if weight is not None else None
-        db = torch.empty_like(bias) if bias is not None else None
-        dgate = torch.empty(x.shape, dtype=x.dtype, device=dev) if gate is not None else None
-        ws = _ws(need, dev)
-        _check(lib.kda_group_norm_bwd(ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(gate), _p(dy), _p(dx), _p(dw),
-                                      _p(db), _p(dgate), _p(ws), need, _stream(dev)))
+    need = lib.kda_group_norm_bwd_workspace_bytes(d) if weight is not None or bias is not None else 0
+    dx, pdx = _new(x, x.shape)
+    dw, pdw = _new_if(weight is not None, x, weight.shape if weight is not None else None, F32)
+    db, pdb = _new_if(bias is not None, x, bias.shape if bias is not None else None, F32)
+    dgate, pdg = _new_if(gate is not None, x, x.shape)
+    ws, pws = _ws(x, need)
+    _launch(dev, lib.kda_group_norm_bwd, d, *ptrs, pdy, pdx, pdw, pdb, pdg, pws, need)
     return dict(dx=dx, dweight=dw, dbias=db, dgate=dgate)
 
 
@@ -424,17 +436,12 @@ def kda_step(q, k, v, g, beta, state, slots=None, scale=None, beta_logits=False)
     dev = _gpu(q, "q")
     if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
         raise ValueError("q must be [B, H, K], v [B, HV, V] and state [S, HV, K, V]")
-    (B, H, K), (HV, V) = q.shape, v.shape[1:]
-    _need(q, "q", q.dtype, (B, H, K), dev)
-    _need(k, "k", q.dtype, (B, H, K), dev)
-    _need(v, "v", q.dtype, (B, HV, V), dev)
-    _need(g, "g", torch.float32, (B, HV, K), dev)
-    _need(beta, "beta", torch.float32, (B, HV), dev)
-    _need(state, "state", torch.float32, (state.shape[0], HV, K, V), dev)
-    _slots(slots, B, dev)
-    d, _ = make_dims(B, 1, H, HV, K, V, 16, scale, "f32" if q.dtype == torch.float32 else "bf16", beta_logits=beta_logits)
-    with _on(dev):
-        o = torch.empty(B, HV, V, dtype=q.dtype, device=dev)
-        _check(_lib().kda_step(ctypes.byref(d), _p(q), _p(k), _p(v), _p(g), _p(beta), _p(slots), state.shape[0], _p(state),
-                               _p(o), _stream(dev)))
+    (B, H, K), (HV, V), S, dt = q.shape, v.shape[1:], state.shape[0], q.dtype
+    ptrs = (_need(q, "q", dt, (B, H, K), dev), _need(k, "k", dt, (B, H, K), dev), _need(v, "v", dt, (B, HV, V), dev),
+            _need(g, "g", F32, (B, HV, K), dev), _need(beta, "beta", F32, (B, HV), dev),
+            _need(slots, "slots", torch.int32, (B,), dev))
+    pst = _need(state, "state", F32, (S, HV, K, V), dev)
+    _, d = _kda_dims(B, H, HV, K, V, scale, "f32" if dt is F32 else "bf16", bool(beta_logits))
+    o, po = _new(q, (B, HV, V))
+    _launch(dev, _lib().kda_step, d, *ptrs, S, pst, po)
     return o

@@ -185,7 +185,10 @@ class _Gpu:
 
     def __init__(self, t):
         self.t = t
-        self.is_cuda, self.device, self.dtype, self.shape = True, "gpu", t.dtype, t.shape
+        self.is_cuda, self.dtype, self.shape = True, t.dtype, t.shape
+
+    def get_device(self):
+        return 0
 
     def __getattr__(self, name):
         return getattr(self.t, name)
@@ -201,10 +204,10 @@ def test_row_strides(make, row):
     t = _Gpu(make())
     if row is None:
         with pytest.raises(ValueError, match="column slice"):
-            layers._rows(t, "x", t.dtype, t.shape, "gpu", 2)
+            layers._rows(t, "x", t.dtype, t.shape, 0, 2)
     else:
-        got = layers._rows(t, "x", t.dtype, t.shape, "gpu", 2)
-        assert got == row
+        got = layers._rows(t, "x", t.dtype, t.shape, 0, 2)
+        assert got == (t.data_ptr(), row)
 
 
 def test_reference_gradients_against_differences():
