@@ -23,6 +23,13 @@ struct Pack {
     if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
     return __uint_as_float(e % 2 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
   }
+  // sets an element of a Pack of zeros
+  __device__ __forceinline__ void put(int e, T x) {
+    if constexpr (sizeof(T) == 4)
+      w[e] = __builtin_bit_cast(uint32_t, x);
+    else
+      w[e / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, x) << (16 * (e % 2));
+  }
 };
 
 // N elements at p; those from `valid` on are zero. `vec`: p is aligned for one load of all N.
@@ -41,12 +48,7 @@ __device__ __forceinline__ Pack<T, N> load_n(const T* p, int valid, bool vec) {
     for (int i = 0; i < Pack<T, N>::WORDS; ++i) r.w[i] = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (i < valid) {
-        if constexpr (sizeof(T) == 4)
-          r.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-        else
-          r.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i % 2));
-      }
+      if (i < valid) r.put(i, p[i]);
   }
   return r;
 }

@@ -27,17 +27,40 @@ __device__ __forceinline__ float item_sum(float x, int tpi, float* sh) {
   return x;
 }
 
-// A lane's share of a group, as loaded.
+// Where a lane's elements are in its group. NEAR (C a multiple of VEC): VEC neighbours a chunk, loaded
+// together where rows are aligned for it (`vec`). Otherwise neighbouring lanes have neighbouring
+// elements, so that loads and stores of single elements cover whole lines (1500 rows of 3 x 333, fp32:
+// 7 against 10 us). The choice goes by C alone: the order of a group's sums, and with it its bits, does
+// not depend on where the tensor lies.
+template <int VEC, bool NEAR>
+struct Place {
+  int lane, tpi, C;
+  bool vec;
+  __device__ __forceinline__ int col(int c, int e) const {
+    return NEAR ? (c * tpi + lane) * VEC + e : (c * VEC + e) * tpi + lane;
+  }
+  __device__ __forceinline__ bool has(int c, int e) const { return NEAR ? col(c, 0) < C : col(c, e) < C; }
+};
+
+// A lane's share of a group, as loaded; zero behind the group's end.
 template <class T, int VEC, int NCH>
 struct Raw {
   Pack<T, VEC> v[NCH];
 
-  __device__ __forceinline__ void load(const void* base, int64_t at, int C, int lane, int tpi, bool vec) {
+  template <bool NEAR>
+  __device__ __forceinline__ void load(const void* base, int64_t at, const Place<VEC, NEAR>& pl) {
     const T* p = static_cast<const T*>(base) + at;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      const int col = (c * tpi + lane) * VEC;
-      v[c] = load_n<T, VEC>(p + col, C - col, vec);
+      if constexpr (NEAR) {
+        v[c] = load_n<T, VEC>(p + pl.col(c, 0), pl.has(c, 0) ? VEC : 0, pl.vec);
+      } else {
+#pragma unroll
+        for (int i = 0; i < Pack<T, VEC>::WORDS; ++i) v[c].w[i] = 0;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (pl.has(c, e)) v[c].put(e, p[pl.col(c, e)]);
+      }
     }
   }
   __device__ __forceinline__ float at(int c, int e) const { return v[c].at(e); }
@@ -60,27 +83,30 @@ struct Act {
   }
 };
 
-template <class T, int VEC, int NCH>
-__device__ __forceinline__ void store_row(void* base, int64_t at, int C, int lane, int tpi, bool vec,
-                                          const float (&in)[NCH][VEC]) {
+template <class T, int VEC, int NCH, bool NEAR>
+__device__ __forceinline__ void store_row(void* base, int64_t at, const Place<VEC, NEAR>& pl, const float (&in)[NCH][VEC]) {
   T* p = static_cast<T*>(base) + at;
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int col = (c * tpi + lane) * VEC;
-    store_n<T, VEC>(p + col, in[c], C - col, vec);
+    if constexpr (NEAR) {
+      store_n<T, VEC>(p + pl.col(c, 0), in[c], pl.has(c, 0) ? VEC : 0, pl.vec);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (pl.has(c, e)) p[pl.col(c, e)] = (T)in[c][e];
+    }
   }
 }
 
-template <int VEC, int NCH>
-__device__ __forceinline__ void load_param(const float* p, float fill, int64_t at, int C, int lane, int tpi, bool vec,
+template <int VEC, int NCH, bool NEAR>
+__device__ __forceinline__ void load_param(const float* p, float fill, int64_t at, const Place<VEC, NEAR>& pl, bool vec,
                                            float (&out)[NCH][VEC]) {
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int col = (c * tpi + lane) * VEC;
-    if (p != nullptr && vec && col + VEC <= C) {
+    if (NEAR && p != nullptr && vec && pl.has(c, 0)) {
 #pragma unroll
       for (int e = 0; e < VEC; e += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p + at + col + e);
+        const float4 v = *reinterpret_cast<const float4*>(p + at + pl.col(c, 0) + e);
         out[c][e] = v.x;
         out[c][e + 1] = v.y;
         out[c][e + 2] = v.z;
@@ -88,14 +114,14 @@ __device__ __forceinline__ void load_param(const float* p, float fill, int64_t a
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) out[c][e] = p != nullptr && col + e < C ? p[at + col + e] : fill;
+      for (int e = 0; e < VEC; ++e) out[c][e] = p != nullptr && pl.has(c, e) ? p[at + pl.col(c, e)] : fill;
     }
   }
 }
 
 // x of a group -> n = (x - mean) rstd; returns rstd. Elements behind the group's end become zero.
-template <int VEC, int NCH>
-__device__ __forceinline__ float normalise(const NormArgs& a, int lane, int tpi, float* sh, float (&x)[NCH][VEC]) {
+template <int VEC, int NCH, bool NEAR>
+__device__ __forceinline__ float normalise(const NormArgs& a, const Place<VEC, NEAR>& pl, float* sh, float (&x)[NCH][VEC]) {
   const float inv = 1.f / (float)a.C;
   if (a.center) {
     float s = 0.f;
@@ -103,13 +129,12 @@ __device__ __forceinline__ float normalise(const NormArgs& a, int lane, int tpi,
     for (int c = 0; c < NCH; ++c)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s += x[c][e];
-    const float mean = item_sum(s, tpi, sh) * inv;
+    const float mean = item_sum(s, pl.tpi, sh) * inv;
 #pragma unroll
     for (int c = 0; c < NCH; ++c)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const int col = (c * tpi + lane) * VEC + e;
-        x[c][e] = col < a.C ? x[c][e] - mean : 0.f;
+        x[c][e] = pl.has(c, e) ? x[c][e] - mean : 0.f;
       }
   }
   float q = 0.f;
@@ -117,7 +142,7 @@ __device__ __forceinline__ float normalise(const NormArgs& a, int lane, int tpi,
   for (int c = 0; c < NCH; ++c)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) q = fmaf(x[c][e], x[c][e], q);
-  const float rstd = 1.f / sqrtf(fmaf(item_sum(q, tpi, sh + 16), inv, a.eps));
+  const float rstd = 1.f / sqrtf(fmaf(item_sum(q, pl.tpi, sh + 16), inv, a.eps));
 #pragma unroll
   for (int c = 0; c < NCH; ++c)
 #pragma unroll
@@ -127,7 +152,7 @@ __device__ __forceinline__ float normalise(const NormArgs& a, int lane, int tpi,
 
 // A group of lanes takes the items sub, sub + stride, ... with stride a multiple of G, so its channels
 // (and the weights in its registers) stay the same; the next item is loaded while this one is worked on.
-template <class T, int VEC, int NCH, int THREADS>
+template <class T, int VEC, int NCH, int THREADS, bool NEAR>
 __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormArgs a, int tpi, int64_t stride) {
   __shared__ float sh[32];
   const int lane = threadIdx.x % tpi;
@@ -135,15 +160,15 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormArgs a, int tpi, 
   const int64_t items = a.R * a.G;
   if (sub >= items) return;  // whole groups of lanes leave; a workgroup-wide group always has its item
   const int g = (int)(sub % a.G);
-  const bool vec = a.vec != 0;
+  const Place<VEC, NEAR> pl{lane, tpi, a.C, a.vec != 0};
   const int64_t pat = a.shared ? 0 : (int64_t)g * a.C, step = stride / a.G;
   int64_t row = sub / a.G;
   Raw<T, VEC, NCH> rx, rg;
-  rx.load(a.x, row * a.x_row + (int64_t)g * a.C, a.C, lane, tpi, vec);
-  if (a.gate != nullptr) rg.load(a.gate, row * a.gate_row + (int64_t)g * a.C, a.C, lane, tpi, vec);
+  rx.load(a.x, row * a.x_row + (int64_t)g * a.C, pl);
+  if (a.gate != nullptr) rg.load(a.gate, row * a.gate_row + (int64_t)g * a.C, pl);
   float w[NCH][VEC], b[NCH][VEC];
-  load_param<VEC, NCH>(a.w, 1.f, pat, a.C, lane, tpi, a.wvec != 0, w);
-  load_param<VEC, NCH>(a.bias, 0.f, pat, a.C, lane, tpi, a.wvec != 0, b);
+  load_param<VEC, NCH, NEAR>(a.w, 1.f, pat, pl, a.wvec != 0, w);
+  load_param<VEC, NCH, NEAR>(a.bias, 0.f, pat, pl, a.wvec != 0, b);
   const Act act(a.act);
   for (; row < a.R; row += step) {
     float x[NCH][VEC];
@@ -153,10 +178,10 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormArgs a, int tpi, 
 #pragma unroll
       for (int e = 0; e < VEC; ++e) x[c][e] = rx.at(c, e);
     if (row + step < a.R) {
-      rx.load(a.x, (row + step) * a.x_row + (int64_t)g * a.C, a.C, lane, tpi, vec);
-      if (a.gate != nullptr) rg.load(a.gate, (row + step) * a.gate_row + (int64_t)g * a.C, a.C, lane, tpi, vec);
+      rx.load(a.x, (row + step) * a.x_row + (int64_t)g * a.C, pl);
+      if (a.gate != nullptr) rg.load(a.gate, (row + step) * a.gate_row + (int64_t)g * a.C, pl);
     }
-    normalise<VEC, NCH>(a, lane, tpi, sh, x);
+    normalise<VEC, NCH, NEAR>(a, pl, sh, x);
     if (a.gate != nullptr) {
 #pragma unroll
       for (int c = 0; c < NCH; ++c)
@@ -168,7 +193,7 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormArgs a, int tpi, 
 #pragma unroll
         for (int e = 0; e < VEC; ++e) x[c][e] = act.value(fmaf(x[c][e], w[c][e], b[c][e]));
     }
-    store_row<T, VEC, NCH>(a.y, (row * a.G + g) * a.C, a.C, lane, tpi, vec, x);
+    store_row<T, VEC, NCH, NEAR>(a.y, (row * a.G + g) * a.C, pl, x);
     if (tpi > 64) __syncthreads();  // the sums' places are read before the next item's are written
   }
 }
@@ -177,13 +202,13 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormArgs a, int tpi, 
 //   dx = rstd (dn - n mean(dn n) - [center] mean(dn)).
 // Partial sums: one row a group of lanes [sub][2][C], or with one weight for all groups one row a
 // workgroup.
-template <class T, int VEC, int NCH, int THREADS>
+template <class T, int VEC, int NCH, int THREADS, bool NEAR>
 __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormArgs a, int tpi, int64_t stride) {
   extern __shared__ float sh[];  // 64 floats, then [groups of lanes][C] where weights are shared
   const int lane = threadIdx.x % tpi, subs = THREADS / tpi;
   const int64_t sub = (int64_t)blockIdx.x * subs + threadIdx.x / tpi;
   const int g = (int)(sub % a.G);
-  const bool vec = a.vec != 0;
+  const Place<VEC, NEAR> pl{lane, tpi, a.C, a.vec != 0};
   const int64_t items = a.R * a.G, step = stride / a.G;
   const float inv = 1.f / (float)a.C;
   float w[NCH][VEC], b[NCH][VEC], dw[NCH][VEC], db[NCH][VEC];
@@ -191,13 +216,13 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormArgs a, int tpi, 
   int64_t row = sub / a.G;
   Raw<T, VEC, NCH> rx, rg, rd;
   auto fetch = [&](int64_t r) {
-    rx.load(a.x, r * a.x_row + (int64_t)g * a.C, a.C, lane, tpi, vec);
-    rd.load(a.dy, (r * a.G + g) * a.C, a.C, lane, tpi, vec);
-    if (a.gate != nullptr) rg.load(a.gate, r * a.gate_row + (int64_t)g * a.C, a.C, lane, tpi, vec);
+    rx.load(a.x, r * a.x_row + (int64_t)g * a.C, pl);
+    rd.load(a.dy, (r * a.G + g) * a.C, pl);
+    if (a.gate != nullptr) rg.load(a.gate, r * a.gate_row + (int64_t)g * a.C, pl);
   };
   if (sub < items) fetch(row);
-  load_param<VEC, NCH>(a.w, 1.f, pat, a.C, lane, tpi, a.wvec != 0, w);
-  load_param<VEC, NCH>(a.bias, 0.f, pat, a.C, lane, tpi, a.wvec != 0, b);
+  load_param<VEC, NCH, NEAR>(a.w, 1.f, pat, pl, a.wvec != 0, w);
+  load_param<VEC, NCH, NEAR>(a.bias, 0.f, pat, pl, a.wvec != 0, b);
   const Act act(a.act);
 #pragma unroll
   for (int c = 0; c < NCH; ++c)
@@ -211,7 +236,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormArgs a, int tpi, 
 #pragma unroll
       for (int e = 0; e < VEC; ++e) x[c][e] = rx.at(c, e);
     if (row + step < a.R) fetch(row + step);
-    const float rstd = normalise<VEC, NCH>(a, lane, tpi, sh, x);
+    const float rstd = normalise<VEC, NCH, NEAR>(a, pl, sh, x);
     const int64_t out = (row * a.G + g) * a.C;
     float s1 = 0.f, s2 = 0.f;
     if (a.gate != nullptr) {
@@ -225,7 +250,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormArgs a, int tpi, 
           dg[c][e] = dy * fmaf(x[c][e], w[c][e], b[c][e]) * d;
           dn[c][e] = dy * v;
         }
-      store_row<T, VEC, NCH>(a.dgate, out, a.C, lane, tpi, vec, dg);
+      store_row<T, VEC, NCH, NEAR>(a.dgate, out, pl, dg);
     } else {
 #pragma unroll
       for (int c = 0; c < NCH; ++c)
@@ -252,7 +277,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormArgs a, int tpi, 
     for (int c = 0; c < NCH; ++c)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) x[c][e] = rstd * (dn[c][e] - s1 - x[c][e] * s2);
-    store_row<T, VEC, NCH>(a.dx, out, a.C, lane, tpi, vec, x);
+    store_row<T, VEC, NCH, NEAR>(a.dx, out, pl, x);
   }
   if (a.part == nullptr) return;
   if (!a.shared || subs == 1) {
@@ -263,8 +288,8 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormArgs a, int tpi, 
     for (int c = 0; c < NCH; ++c)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const int col = (c * tpi + lane) * VEC + e;
-        if (col < a.C) {
+        const int col = pl.col(c, e);
+        if (pl.has(c, e)) {
           p[col] = dw[c][e];
           p[second + col] = db[c][e];
         }
@@ -278,8 +303,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormArgs a, int tpi, 
     for (int c = 0; c < NCH; ++c)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const int col = (c * tpi + lane) * VEC + e;
-        if (col < a.C) acc[(threadIdx.x / tpi) * a.C + col] = k == 0 ? dw[c][e] : db[c][e];
+        if (pl.has(c, e)) acc[(threadIdx.x / tpi) * a.C + pl.col(c, e)] = k == 0 ? dw[c][e] : db[c][e];
       }
     __syncthreads();
     for (int col = threadIdx.x; col < a.C; col += THREADS) {
@@ -321,8 +345,12 @@ __global__ __launch_bounds__(1024) void col_sum_kernel(const float* in, int64_t 
 
 template <class T, int VEC, int NCH, int THREADS>
 hipError_t norm_fwd_t(const NormArgs& a, const NormPlan& p, hipStream_t st) {
-  hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, NCH, THREADS>), dim3((unsigned)p.blocks), dim3(THREADS), 0, st, a, p.tpi,
-                     p.blocks * (THREADS / p.tpi));
+  const dim3 grid((unsigned)p.blocks), block(THREADS);
+  const int64_t stride = p.blocks * (THREADS / p.tpi);
+  if (a.C % VEC == 0)
+    hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, NCH, THREADS, true>), grid, block, 0, st, a, p.tpi, stride);
+  else
+    hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, NCH, THREADS, false>), grid, block, 0, st, a, p.tpi, stride);
   return hipGetLastError();
 }
 
@@ -330,8 +358,12 @@ template <class T, int VEC, int NCH, int THREADS>
 hipError_t norm_bwd_t(const NormArgs& a, const NormPlan& p, hipStream_t st) {
   const int subs = THREADS / p.tpi;
   const size_t lds = sizeof(float) * (64 + (a.shared && subs > 1 ? (size_t)subs * a.C : 0));
-  hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, NCH, THREADS>), dim3((unsigned)p.blocks), dim3(THREADS), lds, st, a, p.tpi,
-                     p.blocks * subs);
+  const dim3 grid((unsigned)p.blocks), block(THREADS);
+  const int64_t stride = p.blocks * subs;
+  if (a.C % VEC == 0)
+    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, NCH, THREADS, true>), grid, block, lds, st, a, p.tpi, stride);
+  else
+    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, NCH, THREADS, false>), grid, block, lds, st, a, p.tpi, stride);
   return hipGetLastError();
 }
 
