@@ -979,24 +979,31 @@ int scan_tiles(int D, int N, int G) {
   return (D / G + ch - 1) / ch;
 }
 
-// Tokens of a segment and of a local one: a cut into about four workgroups a CU (forward) or two
-// (backward, whose registers allow no more), none shorter than 64 tokens. Where the longest sequence is
-// at most two such segments nothing is cut: the pass that a cut needs costs more than the fuller
-// grid gives. Local segments: as short as keeps the first pass within eight workgroups a CU.
+// Tokens of a segment and of a local one. A large call is cut into about four workgroups a CU (forward) or
+// two (backward, whose registers allow no more), and where the longest sequence is at most two such
+// segments not at all: the pass that a cut needs costs more than the fuller grid gives. A call that
+// leaves the chip idle either way is cut for its latency: a chunk takes a workgroup alone 4 us (forward) or
+// 8 (backward), a local segment joined on entry about 0.08, which balances near a quarter of the
+// square root of the length in chunks. Local segments: shorter by up to four while that keeps the first
+// pass within eight workgroups a CU and the joins few.
 void scan_seg(const Seqs& s, int64_t longest, int D, int N, int G, bool bwd, int* seg, int* lseg) {
-  const int64_t cols = (int64_t)G * scan_tiles(D, N, G);
-  const int64_t whole = longest > 0 ? (longest + kScanChunk - 1) / kScanChunk * kScanChunk : kScanChunk;
+  const int64_t cols = (int64_t)G * scan_tiles(D, N, G), C = kScanChunk;
+  const int64_t whole = longest > 0 ? (longest + C - 1) / C * C : C;
   const int64_t want = bwd ? 512 : 1024;
-  int64_t len = (s.total * cols + want - 1) / want;
-  len = (len + 63) / 64 * 64;
-  if (len < 64) len = 64;
-  if (whole <= 2 * len) {
+  int64_t least = 1;
+  while (least * least * 36 * 36 < longest) ++least;  // ceil(sqrt(longest) / 36) chunks
+  least *= C;
+  int64_t len = ((s.total * cols + want - 1) / want + C - 1) / C * C;
+  const bool small = len <= least;
+  if (small) len = least;
+  if (whole <= (small ? 4 : 2) * len) {
     *seg = *lseg = (int)whole;
     return;
   }
+  int64_t r = 1;
+  while (r < 4 && (s.total / len + s.n) * cols * r * 2 <= 2048 && len / (r * 2) >= least) r *= 2;
+  len = (len + C * r - 1) / (C * r) * (C * r);
   *seg = (int)len;
-  int r = 1;
-  while (r < 4 && (s.total / len + s.n) * cols * r * 2 <= 2048) r *= 2;
   *lseg = (int)(len / r);
 }
 
