@@ -259,7 +259,7 @@ kda_status sscan_check(const kda_sscan_dims* d, bool launching, Tokens* t, kda::
   // a local segment has at least 16 tokens, or is a sequence of its own
   if ((t->sq.total / 16 + d->N) * cols > INT32_MAX)
     return fail(KDA_EINVAL, "too many channel tiles (%lld tokens x %lld)", (long long)t->sq.total, (long long)cols);
-  if (t->sq.total * d->G * d->NS / 256 > INT32_MAX) return fail(KDA_EINVAL, "too many tokens for G * NS = %d", d->G * d->NS);
+  if (t->sq.total * d->G * kda::scan_np(d->NS) / 512 + d->D > INT32_MAX) return fail(KDA_EINVAL, "too many tokens for G * NS = %d", d->G * d->NS);
   return KDA_OK;
 }
 
@@ -450,6 +450,8 @@ KDA_EXPORT kda_status kda_sscan_bwd(const kda_sscan_dims* dims, const void* x, c
   scan_use(l, workspace, &a);
   const void* p[7] = {x, dt, z, dy, dx, ddt, dz};
   a.vec = scan_vec(a, dims->dtype, p, 7);
+  const uintptr_t bc = reinterpret_cast<uintptr_t>(dB) | reinterpret_cast<uintptr_t>(dC);
+  a.bcvec = a.N % 4 == 0 && bc % (dims->dtype == KDA_F32 ? 16 : 8) == 0;
   hipStream_t st = static_cast<hipStream_t>(stream);
   TRY(scan_tables(dims, l, workspace, a, st));
   return hip_status(kda::launch_sscan_bwd(dims->dtype, a, st), "kda_sscan_bwd");

@@ -75,6 +75,7 @@ struct ScanArgs {
   float* part_a;            // bwd [nseg][D][NP]
   float* part_d;            // bwd [nseg][2][D]: dskip, ddt_bias
   int vec;                  // rows allow four-element loads
+  int bcvec;                // rows of dB and dC allow four-element stores
 };
 int scan_np(int N);                      // padded states
 int scan_tiles(int D, int N, int G);     // channel tiles of one group

@@ -759,35 +759,47 @@ __global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles
   }
 }
 
-// dB and dC from the channel tiles' sums.
+// Joins the partial sums of a backward. The first bc_blocks workgroups: dB and dC from the channel tiles, four
+// states a thread. The others: dA [D][N], dskip [D], ddt_bias [D] from the segments, 64 columns a
+// workgroup with the segments dealt to 4 lanes a column. Fixed orders throughout.
 template <class T, int NP>
-__global__ __launch_bounds__(256) void sscan_bc_kernel(ScanArgs a, int tiles) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // (token, group, state)
-  const int64_t rows = a.sq.total * a.G;
-  if (i >= rows * a.N) return;
-  const int64_t row = i / a.N;
-  const int n = (int)(i % a.N);
-  float c = 0.f, b = 0.f;
-  for (int t = 0; t < tiles; ++t) {
-    const float* p = a.part_bc + ((int64_t)t * rows + row) * 2 * NP;
-    c += p[n];
-    b += p[NP + n];
-  }
-  static_cast<T*>(a.dC)[i] = (T)c;
-  static_cast<T*>(a.dB)[i] = (T)b;
-}
-
-// dA [D][N], dskip [D], ddt_bias [D] from the segments' sums: 64 columns a workgroup, the segments
-// dealt to 4 lanes a column.
-__global__ __launch_bounds__(256) void sscan_param_kernel(ScanArgs a, int NP) {
+__global__ __launch_bounds__(256) void sscan_sums_kernel(ScanArgs a, int tiles, int64_t bc_blocks) {
   __shared__ float sh[4][64];
+  if ((int64_t)blockIdx.x < bc_blocks) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t rows = a.sq.total * a.G, row = i / (NP / 2);
+    if (row >= rows) return;
+    const int v = (int)(i % (NP / 2)) * 4, n = v % NP;  // the first NP of a row's 2 NP are dC
+    const float4* p = reinterpret_cast<const float4*>(a.part_bc + row * 2 * NP + v);
+    const int64_t step = rows * (NP / 2);
+    float s[4] = {};
+    for (int t = 0; t < tiles; t += 8) {
+      float4 r[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (t + u < tiles) r[u] = p[(t + u) * step];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (t + u < tiles) {
+          s[0] += r[u].x;
+          s[1] += r[u].y;
+          s[2] += r[u].z;
+          s[3] += r[u].w;
+        }
+    }
+    T* out = static_cast<T*>(v < NP ? a.dC : a.dB) + row * a.N + n;
+    store_n<T, 4>(out, s, a.N - n, a.bcvec != 0);
+    return;
+  }
   const int tx = threadIdx.x % 64, ty = threadIdx.x / 64;
-  const int64_t col = (int64_t)blockIdx.x * 64 + tx, na = (int64_t)a.D * NP, cols = na + 2 * (int64_t)a.D;
+  const int64_t col = ((int64_t)blockIdx.x - bc_blocks) * 64 + tx, na = (int64_t)a.D * NP, cols = na + 2 * (int64_t)a.D;
   const float* p = col < na ? a.part_a + col : a.part_d + (col - na);
   const int64_t stride = col < na ? na : 2 * (int64_t)a.D;
   float s = 0.f;
-  if (col < cols)
+  if (col < cols) {
+#pragma unroll 4
     for (int64_t r = ty; r < a.nseg; r += 4) s += p[r * stride];
+  }
   sh[ty][tx] = s;
   __syncthreads();
   if (ty != 0 || col >= cols) return;
@@ -817,7 +829,7 @@ __global__ __launch_bounds__(1024) void sscan_tables_kernel(const int32_t* cu, i
       sh[k][threadIdx.x] = mine[k];
     }
     __syncthreads();
-    for (int step = 1; step < 1024; step *= 2) {
+    for (int step = 1; step < min(n - i0, 1024); step *= 2) {
       int add[3];
 #pragma unroll
       for (int k = 0; k < 3; ++k) add[k] = (int)threadIdx.x >= step ? sh[k][threadIdx.x - step] : 0;
@@ -829,7 +841,7 @@ __global__ __launch_bounds__(1024) void sscan_tables_kernel(const int32_t* cu, i
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       if (i < n) out[k][i] = base[k] + sh[k][threadIdx.x] - mine[k];
-      base[k] += sh[k][1023];
+      base[k] += sh[k][min(n - i0, 1024) - 1];
     }
     __syncthreads();
   }
@@ -932,12 +944,8 @@ hipError_t bwd_np(const ScanArgs& a, hipStream_t st) {
   else
     hipLaunchKernelGGL((sscan_bwd_kernel<T, NP, false>), grid, dim3(256), 0, st, a, tiles);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  const int64_t bc = a.sq.total * a.G * a.N;
-  if (bc > 0) {
-    hipLaunchKernelGGL((sscan_bc_kernel<T, NP>), dim3((unsigned)((bc + 255) / 256)), dim3(256), 0, st, a, tiles);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL(sscan_param_kernel, dim3((unsigned)(((int64_t)a.D * (NP + 2) + 63) / 64)), dim3(256), 0, st, a, NP);
+  const int64_t bc = (a.sq.total * a.G * (NP / 2) + 255) / 256, par = ((int64_t)a.D * (NP + 2) + 63) / 64;
+  hipLaunchKernelGGL((sscan_sums_kernel<T, NP>), dim3((unsigned)(bc + par)), dim3(256), 0, st, a, tiles, bc);
   return hipGetLastError();
 }
 
