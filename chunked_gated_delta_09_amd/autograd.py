@@ -16,6 +16,7 @@ workspace and dO).
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import chunk_bwd, fwd_states, layers
 
@@ -72,6 +73,7 @@ class ShortConvFunction(torch.autograd.Function):
         return f["y"], f["final_state"]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dfinal):
         x, weight, bias, h0, cu_dev = ctx.saved_tensors
         dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
@@ -100,6 +102,7 @@ class SelectiveScanFunction(torch.autograd.Function):
         return f["y"], f["final_state"]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dfinal):
         x, dt, A, B, C, skip, z, dt_bias, cu_dev, states = ctx.saved_tensors
         dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
@@ -129,6 +132,7 @@ class GroupNormFunction(torch.autograd.Function):
         return layers.group_norm(x, groups, weight=weight, bias=bias, gate=gate, **ctx.args)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, bias, gate = ctx.saved_tensors
         r = layers.group_norm_bwd(x, ctx.groups, dy.contiguous(), weight=weight, bias=bias, gate=gate, **ctx.args)

@@ -32,6 +32,7 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 // Offsets into arrays of states and tokens are 64 bits wide in the kernels; what is limited are the
 // grids (one dimension of workgroups) and the 32-bit token numbers of cu_seqlens.
 constexpr int64_t kMaxTokens = INT32_MAX - 64;
+constexpr int64_t kMaxBlocks = (1 << 24) - 1;  // workgroups of 256: fewer than 2^32 threads
 constexpr int kMaxChannels = 1 << 20;
 constexpr int64_t kMaxRow = 1 << 25;
 constexpr int kMaxStepRows = 65535;  // second grid dimension
@@ -127,6 +128,8 @@ kda_status conv_check(const kda_conv_dims* d, bool launching, Tokens* t, kda::Co
   TRY(check_dtype(d->dtype));
   *a = kda::ConvArgs{};
   TRY(row_of(d->x_row, d->D, "x", &a->x_row));
+  // a run has at least 8 tokens, 64 where there are enough of them
+  if (t->sq.total / 64 + d->N + (1 << 20) > kMaxBlocks) return fail(KDA_EINVAL, "too many tokens (%lld)", (long long)t->sq.total);
   a->sq = t->sq;
   a->D = d->D;
   a->W = d->W;
@@ -257,9 +260,9 @@ kda_status sscan_check(const kda_sscan_dims* d, bool launching, Tokens* t, kda::
   a->softplus = d->softplus;
   const int64_t cols = (int64_t)d->G * kda::scan_tiles(d->D, d->NS, d->G);
   // a local segment has at least 16 tokens, or is a sequence of its own
-  if ((t->sq.total / 16 + d->N) * cols > INT32_MAX)
+  if ((t->sq.total / 16 + d->N) * cols > kMaxBlocks)
     return fail(KDA_EINVAL, "too many channel tiles (%lld tokens x %lld)", (long long)t->sq.total, (long long)cols);
-  if (t->sq.total * d->G * kda::scan_np(d->NS) / 512 + d->D > INT32_MAX) return fail(KDA_EINVAL, "too many tokens for G * NS = %d", d->G * d->NS);
+  if (t->sq.total * d->G * kda::scan_np(d->NS) / 512 + 2 * (int64_t)d->D > kMaxBlocks) return fail(KDA_EINVAL, "too many tokens for G * NS = %d", d->G * d->NS);
   return KDA_OK;
 }
 

@@ -568,10 +568,12 @@ __global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles
     float h0[NPL], dAc[NPL];
 #pragma unroll
     for (int k = 0; k < L::ITEMS; ++k) {
-      kx[k] = rx[k];
-      kd[k] = rd[k];
-      kz[k] = rz[k];
-      ky[k] = ry[k];
+      if (L::ITEMS == 1) {
+        kx[k] = rx[k];
+        kd[k] = rd[k];
+        kz[k] = rz[k];
+        ky[k] = ry[k];
+      }
       if (sv.has(k)) {
         const bool ok = sv.token(k) < live;
         float bias[4], g4[4];
@@ -698,6 +700,13 @@ __global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles
 #pragma unroll
     for (int k = 0; k < L::ITEMS; ++k)
       if (sv.has(k)) {
+        if (L::ITEMS > 1) {  // with two pieces a thread there are no registers to keep them over the walk
+          const int64_t t = sg.t0 + at;
+          kx[k] = sv.load(a.x, t, a.x_row, ox[k], k, live);
+          kd[k] = sv.load(a.dt, t, a.dt_row, od[k], k, live);
+          ky[k] = sv.load(a.dy, t, a.D, oy[k], k, live);
+          if (GATE) kz[k] = sv.load(a.z, t, a.z_row, oz[k], k, live);
+        }
         const int pt = sv.token(k), pc = sv.col(k);
         float vx[4], vd[4], vz[4], s1[4], s2[4], y[4], skip[4], bias[4];
         unpack(*reinterpret_cast<const float4*>(&sG[pt][pc]), s1);

@@ -208,7 +208,11 @@ def _ws(like, n):
 
 
 def _new(like, shape, dtype=None):
-    t = like.new_empty(shape, dtype=dtype)
+    """A contiguous tensor of this shape, of the type (but for `dtype`) and on the GPU of `like`, and its address."""
+    if dtype is None and like.shape == shape and like.is_contiguous():
+        t = torch.empty_like(like)
+    else:
+        t = like.new_empty(shape, dtype=dtype)
     return t, t.data_ptr()
 
 
@@ -442,6 +446,6 @@ def kda_step(q, k, v, g, beta, state, slots=None, scale=None, beta_logits=False)
             _need(slots, "slots", torch.int32, (B,), dev))
     pst = _need(state, "state", F32, (S, HV, K, V), dev)
     _, d = _kda_dims(B, H, HV, K, V, scale, "f32" if dt is F32 else "bf16", bool(beta_logits))
-    o, po = _new(q, (B, HV, V))
+    o, po = _new(v, (B, HV, V))
     _launch(dev, _lib().kda_step, d, *ptrs, S, pst, po)
     return o

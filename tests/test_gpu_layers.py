@@ -517,3 +517,120 @@ def test_two_streams_at_once():
     for i in range(2):
         for a, b in zip(got[i], want[i]):
             assert torch.equal(a, b)
+
+
+# ---- edges
+
+
+def test_no_tokens():
+    """T = 0: states pass through, gradients of parameters are zero."""
+    d = Draw(61)
+    D, NS = 24, 16
+    x = torch.empty(2, 0, D, device="cuda")
+    w, h = d(D, 4)[0], d(2, 3, D)[0]
+    f = layers.short_conv(x, w, h0=h, output_final_state=True)
+    b = layers.short_conv_bwd(x, w, x, h0=h, dfinal=h)
+    assert f["y"].shape == (2, 0, D) and torch.equal(f["final_state"], h)
+    assert torch.equal(b["dh0"], h) and not b["dweight"].any()
+    A, h0, bc = -torch.ones(D, NS, device="cuda"), d(2, D, NS)[0], torch.empty(2, 0, 1, NS, device="cuda")
+    f = layers.selective_scan(x, x, A, bc, bc, skip=w[:, 0].contiguous(), h0=h0, save=True)
+    b = layers.selective_scan_bwd(x, x, A, bc, bc, f["states"], x, skip=w[:, 0].contiguous(), dfinal=h0, output_dh0=True)
+    assert torch.equal(f["final_state"], h0) and torch.equal(b["dh0"], h0)
+    assert not b["dA"].any() and not b["dskip"].any()
+
+
+def test_many_short_sequences():
+    """More sequences than a table's workgroup has lanes, most of them empty or a token long."""
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 4, (1500,), generator=g)
+    cu = [0] + torch.cumsum(lens, 0).tolist()
+    T, D, NS, N = cu[-1], 12, 8, 1500
+    v, d = scan_inputs(63, F32, 1, T, D, NS, 1, N, "softplus skip gate state")
+    dy, dy64 = d(1, T, D, leaf=False)
+    df, df64 = d(N, D, NS, leaf=False)
+    dev = {k: t[0] for k, t in v.items()}
+    y64, f64 = ref.scan(*(v[k][1] for k in ("x", "dt", "A", "B", "C", "skip", "z", "dt_bias", "h0")), True, cu)
+    names = [k for k in v if v[k][1] is not None]
+    gr = dict(zip(names, grads((y64, f64), (dy64, df64), [v[k][1] for k in names])))
+    f = layers.selective_scan(**dev, cu_seqlens=cu, dt_softplus=True, save=True)
+    dev.pop("h0")
+    r = layers.selective_scan_bwd(**dev, states=f["states"], dy=dy, dfinal=df, cu_seqlens=cu, dt_softplus=True, output_dh0=True)
+    ref.close(f["y"], y64, F32, ops(4), "y")
+    ref.close(f["final_state"], f64, F32, ops(4), "final_state")
+    out = dict(x="dx", dt="ddt", A="dA", B="dB", C="dC", skip="dskip", z="dz", h0="dh0")
+    for k in names:
+        ref.close(r[out[k]], gr[k], F32, ops(T if k in ("A", "skip") else 4), out[k])
+    w, w64 = d(D, 4)
+    h, h64 = d(N, 3, D)
+    y64, f64 = ref.conv(v["x"][1], w64, None, h64, "silu", cu)
+    gw, gh = grads((y64,), (dy64,), [w64, h64])
+    f = layers.short_conv(v["x"][0], w, h0=h, cu_seqlens=cu, output_final_state=True)
+    b = layers.short_conv_bwd(v["x"][0], w, dy, h0=h, cu_seqlens=cu)
+    ref.close(f["y"], y64, F32, 64, "y")
+    ref.close(b["dweight"], gw, F32, ops(T), "dweight")
+    ref.close(b["dh0"], gh, F32, 64, "dh0")
+
+
+def test_masked_neighbours_do_not_leak():
+    """NaN and infinity in one sequence's inputs and states stay in that sequence."""
+    cu, T, D, NS = [0, 9, 30, 41], 41, 16, 8
+    v, d = scan_inputs(67, F32, 1, T, D, NS, 1, 3, "softplus gate state")
+    dev = {k: t[0] for k, t in v.items()}
+    w, h = d(D, 4)[0], d(3, 3, D)[0]
+    dy = d(1, T, D)[0]
+
+    def run():
+        f = layers.short_conv(dev["x"], w, h0=h, cu_seqlens=cu, output_final_state=True)
+        b = layers.short_conv_bwd(dev["x"], w, dy, h0=h, cu_seqlens=cu)
+        s = layers.selective_scan(**dev, cu_seqlens=cu, dt_softplus=True, save=True)
+        kw = {k: t for k, t in dev.items() if k != "h0"}
+        g = layers.selective_scan_bwd(**kw, states=s["states"], dy=dy, cu_seqlens=cu, dt_softplus=True, output_dh0=True)
+        rows = [f["y"][0], b["dx"][0], s["y"][0]] + [g[k][0] for k in ("dx", "ddt", "dz", "dB", "dC")]
+        return rows, [f["final_state"], b["dh0"], s["final_state"], g["dh0"]]
+
+    clean = run()
+    for k in ("x", "dt", "z", "B", "C"):
+        dev[k][0, 9:30] = float("nan") if k != "z" else float("inf")
+    dy[0, 9:30] = float("nan")
+    h[1], dev["h0"][1] = float("inf"), float("nan")
+    dirty = run()
+    keep = torch.cat([torch.arange(9), torch.arange(30, 41)]).cuda()
+    for a, b in zip(clean[0], dirty[0]):
+        assert torch.equal(a[keep], b[keep])
+    for a, b in zip(clean[1], dirty[1]):
+        assert torch.equal(a[[0, 2]], b[[0, 2]])
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: the last rows against a run of their own."""
+    D, T = 4096, 2 ** 19 + 40
+    x = torch.empty(1, T, D, dtype=BF16, device="cuda").uniform_(-1, 1, generator=torch.Generator("cuda").manual_seed(5))
+    assert x.numel() > 2 ** 31
+    w = torch.rand(D, 4, device="cuda") - 0.5
+    tail = x[:, -200:].contiguous()
+    y, small = layers.short_conv(x, w)["y"], layers.short_conv(tail, w)["y"]
+    assert torch.equal(y[:, -100:], small[:, -100:])
+    del y
+    dx, small = layers.short_conv_bwd(x, w, x)["dx"], layers.short_conv_bwd(tail, w, tail)["dx"]
+    assert torch.equal(dx[:, -100:], small[:, -100:])
+    del dx
+    gate = x.view(-1, 32, 128)
+    y = layers.group_norm(x, 32, gate=x, activation="silu")
+    assert torch.equal(y[:, -100:], layers.group_norm(tail, 32, gate=tail, activation="silu")[:, -100:])
+    del y, gate
+    # decays of e^-2 a token and more: 100 tokens on, nothing is left of an earlier state
+    A = -torch.arange(2, 10, device="cuda", dtype=F32).expand(D, 8).contiguous()
+    bc = torch.ones(1, T, 1, 8, dtype=BF16, device="cuda")
+    step = torch.ones_like(x)
+    y = layers.selective_scan(x, step, A, bc, bc)["y"]
+    small = layers.selective_scan(tail, step[:, -200:].contiguous(), A, bc[:, -200:].contiguous(), bc[:, -200:].contiguous())["y"]
+    # both within half a step of bf16 of sums of at most 8 terms that fp32 holds to 2^-20
+    ref.close(y[:, -100:], small[:, -100:].cpu(), BF16, 64)
+    del x, y, step
+    state = torch.zeros(33000, 1, 256, 256, device="cuda")
+    assert state.numel() > 2 ** 31
+    state[-1] = 1.0
+    q = torch.ones(1, 1, 256, device="cuda")
+    o = layers.kda_step(q, q * 0, q, q * 0, torch.ones(1, 1, device="cuda"), state, scale=1.0,
+                        slots=torch.tensor([32999], dtype=torch.int32, device="cuda"))
+    assert torch.equal(o, torch.full_like(o, 256.0)) and not state[0].any()
