@@ -290,8 +290,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t run_b
       }
     };
     for (int t = t0; t < t1 + W - 1; t += kAhead) {
-      if (t - (W - 1) >= t0 && t - (W - 1) >= c.begin && t + kAhead + (W - 1) < c.end && t + kAhead <= t1) {
-        // inside the run, and the tokens that get whole are clear of both ends of the sequence
+      if (t - (W - 1) >= c.begin && t + kAhead + (W - 1) < c.end && t + kAhead <= t1) {
+        // the run's own tokens, and those that get whole are clear of both ends of the sequence
         Pack<T, VEC> in[kAhead], g[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
@@ -302,7 +302,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t run_b
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           token(in[i], g[i], 0, 1.f);
-          store_n<T, VEC>(dx + (int64_t)(t + i - (W - 1)) * a.D, pend[0], valid, VEC > 1);
+          if (t + i - (W - 1) >= t0) store_n<T, VEC>(dx + (int64_t)(t + i - (W - 1)) * a.D, pend[0], valid, VEC > 1);
         }
       } else {
         fetch(t + kAhead);
