@@ -285,7 +285,7 @@ ScanLayout scan_layout(const kda_sscan_dims* d, const Tokens& t, bool bwd) {
   }
   const size_t NP = kda::scan_np(d->NS), D = d->D;
   size_t o = 0;
-  if (d->cu_seqlens_host != nullptr) {
+  if (d->cu_seqlens_host != nullptr && d->N > kda::kScanLanes) {
     l.segoff = o; o = align_up(o + sizeof(int32_t) * (d->N + 1));
     l.loff = o; o = align_up(o + sizeof(int32_t) * (d->N + 1));
     l.choff = o; o = align_up(o + sizeof(int32_t) * (d->N + 1));
@@ -329,7 +329,7 @@ int scan_vec(const kda::ScanArgs& a, int dtype, const void* const* ptrs, int np)
 }
 
 kda_status scan_tables(const kda_sscan_dims* d, const ScanLayout& l, void* workspace, const kda::ScanArgs& a, hipStream_t st) {
-  if (d->cu_seqlens_host == nullptr) return KDA_OK;
+  if (d->cu_seqlens_host == nullptr || d->N <= kda::kScanLanes) return KDA_OK;
   char* ws = static_cast<char*>(workspace);
   return hip_status(kda::launch_scan_tables(a.sq, l.seg, l.lseg, reinterpret_cast<int32_t*>(ws + l.segoff),
                                             reinterpret_cast<int32_t*>(ws + l.loff),

@@ -50,6 +50,8 @@ hipError_t launch_conv_step(int dtype, const ConvStepArgs& a, hipStream_t st);
 constexpr int kScanStates = 4;
 // Tokens of a chunk: the forward saves the state entering each, the backward walks them in reverse.
 constexpr int kScanChunk = KDA_SCAN_CHUNK;
+// Packed sequences that a wave counts by itself; more have tables in the workspace.
+constexpr int kScanLanes = 64;
 
 struct ScanArgs {
   Seqs sq;
@@ -63,12 +65,12 @@ struct ScanArgs {
   // segments: every sequence is cut into max(1, ceil(len / seg)) runs of seg tokens
   int seg;                  // tokens of a segment (a multiple of the chunk)
   int64_t nseg;             // segments in all
-  const int32_t* segoff;    // packed: [n + 1] first segment of each sequence
-  const int32_t* choff;     // packed: [n + 1] first chunk of each sequence
+  const int32_t* segoff;    // more than kScanLanes packed: [n + 1] first segment of each sequence
+  const int32_t* choff;     // likewise its first chunk
   int split;                // some sequence has more than one segment
   int lseg;                 // tokens of a local segment (divides seg)
   int64_t nloc;             // local segments in all
-  const int32_t* loff;      // packed: [n + 1] first local segment of each sequence
+  const int32_t* loff;      // likewise its first local segment
   float* seg_dt;            // [nloc][D] sum of dt over the local segment
   float* seg_state;         // [nloc][D][NP] what the local segment adds to the carried state
   float* part_bc;           // bwd [tiles of a group][tokens][G][2 NP]

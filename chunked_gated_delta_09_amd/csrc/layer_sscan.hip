@@ -32,37 +32,61 @@ struct Segment {
   int n;               // sequence
   int j, count;        // place among the sequence's segments of this length, their number
   int64_t first;       // the first of them
+  int64_t first_local; // the sequence's first local segment (lseg tokens each)
+  int64_t first_chunk; // the sequence's first chunk
   int64_t t0;          // first token
   int len;             // tokens
 };
 
 // Segments of `seg` tokens in a sequence of `len`.
 __device__ __forceinline__ int segments_of(int64_t len, int seg) { return len > 0 ? (int)((len + seg - 1) / seg) : 1; }
+__device__ __forceinline__ int chunks_of(int64_t len) { return (int)((len + TT - 1) / TT); }
 
-// Segment s of length seg; off: the first segment of each packed sequence.
-__device__ __forceinline__ Segment segment_at(const Seqs& sq, int64_t s, int seg, const int32_t* off) {
+// Segment s (LOCAL: local segment s). Of packed sequences up to 64 each wave counts their segments itself, a
+// sequence a lane; more have tables from a kernel before this one (which costs a small call 4 us).
+template <bool LOCAL>
+__device__ __forceinline__ Segment segment_at(const ScanArgs& a, int64_t s) {
   Segment g;
-  if (sq.cu != nullptr) {
-    g.n = find_seq(off, sq.n, s);
-    g.first = off[g.n];
-    g.count = (int)(off[g.n + 1] - g.first);
-  } else {
-    g.count = segments_of(sq.T, seg);
+  const int seg = LOCAL ? a.lseg : a.seg;
+  if (a.sq.cu == nullptr) {
+    g.count = segments_of(a.sq.T, seg);
     g.n = (int)(s / g.count);
     g.first = (int64_t)g.n * g.count;
+    g.first_local = (int64_t)g.n * segments_of(a.sq.T, a.lseg);
+    g.first_chunk = (int64_t)g.n * chunks_of(a.sq.T);
+  } else if (a.sq.n > kScanLanes) {
+    const int32_t* off = LOCAL ? a.loff : a.segoff;
+    g.n = find_seq(off, a.sq.n, s);
+    g.first = off[g.n];
+    g.count = (int)(off[g.n + 1] - g.first);
+    g.first_local = a.loff[g.n];
+    g.first_chunk = a.choff[g.n];
+  } else {
+    const int lane = threadIdx.x % 64;
+    const bool has = lane < a.sq.n;
+    const int len = has ? a.sq.cu[lane + 1] - a.sq.cu[lane] : 0;
+    const int mine[3] = {has ? segments_of(len, a.seg) : 0, has ? segments_of(len, a.lseg) : 0, has ? chunks_of(len) : 0};
+    int upto[3] = {mine[0], mine[1], mine[2]};
+#pragma unroll
+    for (int step = 1; step < 64; step *= 2)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const int below = __shfl_up(upto[k], step, 64);
+        if (lane >= step) upto[k] += below;
+      }
+    const int w = LOCAL ? 1 : 0;
+    g.n = __ffsll((unsigned long long)__ballot(has && upto[w] > s)) - 1;
+    const int at = __builtin_amdgcn_readfirstlane(g.n);
+    g.n = at;
+    g.first = __builtin_amdgcn_readlane(upto[w] - mine[w], at);
+    g.count = __builtin_amdgcn_readlane(mine[w], at);
+    g.first_local = __builtin_amdgcn_readlane(upto[1] - mine[1], at);
+    g.first_chunk = __builtin_amdgcn_readlane(upto[2] - mine[2], at);
   }
   g.j = (int)(s - g.first);
-  g.t0 = seq_begin(sq, g.n) + (int64_t)g.j * seg;
-  g.len = (int)min((int64_t)seg, seq_end(sq, g.n) - g.t0);
+  g.t0 = seq_begin(a.sq, g.n) + (int64_t)g.j * seg;
+  g.len = (int)min((int64_t)seg, seq_end(a.sq, g.n) - g.t0);
   return g;
-}
-__device__ __forceinline__ int64_t first_chunk(const ScanArgs& a, const Segment& g) {
-  const int64_t first = a.sq.cu != nullptr ? a.choff[g.n] : (int64_t)g.n * ((a.sq.T + TT - 1) / TT);
-  return first + (int64_t)g.j * (a.seg / TT);
-}
-// A sequence's local segments (lseg tokens each).
-__device__ __forceinline__ int64_t first_local(const ScanArgs& a, int n) {
-  return a.sq.cu != nullptr ? a.loff[n] : (int64_t)n * segments_of(a.sq.T, a.lseg);
 }
 
 // What a workgroup's lanes are.
@@ -240,7 +264,7 @@ __global__ __launch_bounds__(256) void sscan_fwd_kernel(ScanArgs a, int tiles) {
   __shared__ float sBias[L::CH], sSkip[L::CH];
   const int bx = blockIdx.x % (a.G * tiles), grp = bx / tiles;
   const int c0 = (bx % tiles) * L::CH;      // first channel, within the group
-  const Segment sg = segment_at(a.sq, blockIdx.x / (a.G * tiles), OUT ? a.seg : a.lseg, OUT ? a.segoff : a.loff);
+  const Segment sg = segment_at<!OUT>(a, blockIdx.x / (a.G * tiles));
   // the last segment of the second pass has no successor to carry its state to
   if (!OUT && sg.j >= (segments_of(seq_end(a.sq, sg.n) - seq_begin(a.sq, sg.n), a.seg) - 1) * (a.seg / a.lseg)) return;
   Stage<T, NP> sv(a, grp, c0);
@@ -258,9 +282,9 @@ __global__ __launch_bounds__(256) void sscan_fwd_kernel(ScanArgs a, int tiles) {
   if (OUT) {
     if (a.h0 != nullptr) load_states<NP>(a.h0, (int64_t)sg.n * a.D + d, a.N, part, in, h);
     if (in && a.split)
-      join_segments<NP>(a, first_local(a, sg.n), 1, (int64_t)sg.j * (a.seg / a.lseg), d, part, A2, h);
+      join_segments<NP>(a, sg.first_local, 1, (int64_t)sg.j * (a.seg / a.lseg), d, part, A2, h);
   }
-  const int64_t chunk0 = OUT ? first_chunk(a, sg) : 0;
+  const int64_t chunk0 = sg.first_chunk + (int64_t)sg.j * (a.seg / TT);
   float total[L::ITEMS][4] = {};  // sum of dt over the tokens that this thread stages
   sv.params(a.dt_bias, sBias);
   if (OUT) sv.params(a.skip, sSkip);
@@ -379,7 +403,7 @@ __global__ __launch_bounds__(256) void sscan_bwd_local_kernel(ScanArgs a, int ti
   __shared__ float sBias[L::CH];
   const int bx = blockIdx.x % (a.G * tiles), grp = bx / tiles;
   const int c0 = (bx % tiles) * L::CH;
-  const Segment sg = segment_at(a.sq, blockIdx.x / (a.G * tiles), a.lseg, a.loff);
+  const Segment sg = segment_at<true>(a, blockIdx.x / (a.G * tiles));
   if (sg.j < a.seg / a.lseg) return;  // the first segment of the second pass has no predecessor
   Stage<T, NP> sv(a, grp, c0);
   const int tid = threadIdx.x, part = tid % L::LPC, chl = tid / L::LPC;
@@ -506,7 +530,7 @@ __global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles
   __shared__ float sBias[L::CH], sSkip[L::CH];
   const int bx = blockIdx.x % (a.G * tiles), grp = bx / tiles, tile = bx % tiles;
   const int c0 = tile * L::CH;
-  const Segment sg = segment_at(a.sq, blockIdx.x / (a.G * tiles), a.seg, a.segoff);
+  const Segment sg = segment_at<false>(a, blockIdx.x / (a.G * tiles));
   Stage<T, NP> sv(a, grp, c0);
   const int tid = threadIdx.x, part = tid % L::LPC, chl = tid / L::LPC, lane = tid % 64, wave = tid / 64;
   const bool in = c0 + chl < sv.per;
@@ -521,9 +545,9 @@ __global__ __launch_bounds__(256, 2) void sscan_bwd_kernel(ScanArgs a, int tiles
   if (a.dfinal != nullptr) load_states<NP>(a.dfinal, (int64_t)sg.n * a.D + d, a.N, part, in, q);
   if (in && a.split) {
     const int64_t count = segments_of(seq_end(a.sq, sg.n) - seq_begin(a.sq, sg.n), a.lseg);
-    join_segments<NP>(a, first_local(a, sg.n) + count - 1, -1, count - (int64_t)(sg.j + 1) * (a.seg / a.lseg), d, part, A2, q);
+    join_segments<NP>(a, sg.first_local + count - 1, -1, count - (int64_t)(sg.j + 1) * (a.seg / a.lseg), d, part, A2, q);
   }
-  const int64_t chunk0 = first_chunk(a, sg);
+  const int64_t chunk0 = sg.first_chunk + (int64_t)sg.j * (a.seg / TT);
   sv.params(a.dt_bias, sBias);
   sv.params(a.skip, sSkip);
   // where a lane's sum over channels goes: bit 5 dC or dB, bits 4 and 3 the state of its four
@@ -838,7 +862,7 @@ __global__ __launch_bounds__(1024) void sscan_tables_kernel(const int32_t* cu, i
   for (int i0 = 0; i0 < n; i0 += 1024) {
     const int i = i0 + threadIdx.x;
     const int len = i < n ? cu[i + 1] - cu[i] : 0;
-    int mine[3] = {segments_of(len, seg), segments_of(len, lseg), (len + TT - 1) / TT};
+    int mine[3] = {segments_of(len, seg), segments_of(len, lseg), chunks_of(len)};
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       if (i >= n) mine[k] = 0;

@@ -131,9 +131,11 @@ def test_selective_scan(dtype, seqs, D, NS, G, opts):
     assert all((r[out[k]] is None) == (v[k][1] is None) for k in ("skip", "z", "dt_bias", "h0"))
 
 
-@pytest.mark.parametrize("cu", [None, [0, 5, 5, 905, 1000]], ids=["dense", "packed"])
+@pytest.mark.parametrize("cu", [None, [0, 5, 5, 905, 1000], [0] * 10 + list(range(60)) + [959, 960, 1000]],
+                         ids=["dense", "packed", "packed_tables"])
 def test_selective_scan_cut_sequences(cu):
-    """Few channels and long sequences: the scan is cut along the tokens (the workspace says so)."""
+    """Few channels and long sequences: the scan is cut along the tokens. Up to 64 packed sequences are
+    counted by each wave, more (the last case) by tables."""
     B, T, D, NS = 1, 1000, 64, 16
     N = len(cu) - 1 if cu else 1
     opts = "softplus dt_bias gate skip state"
