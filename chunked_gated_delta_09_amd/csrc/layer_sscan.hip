@@ -512,7 +512,8 @@ __device__ __forceinline__ float merge(float x, float y, int lane) {
 //   dx = dt sum_n r B + skip dy',   ddt = x sum_n r B + sum_n A p,   dz = dy y' silu'(z).
 // Halves keep the states and decays of 8 tokens in registers rather than 16 (64 values a lane less), for
 // the recurrence of the first 8 run twice: 166 us against 201 (B=2, T=2048, D=2048, N=16, bf16). Three waves
-// a SIMD instead of two (168 registers, 64 spilled) took 279. The sums over channels are joined over the wave's lanes by
+// a SIMD instead of two: 279 with halves (168 registers, 64 spilled), 153 against 145 with quarters, which
+// fit but form the states of 12 tokens twice. The sums over channels are joined over the wave's lanes by
 // merges (half the values move at each step), over the four waves in shared memory, and over
 // channel tiles by a second kernel.
 template <class T, int NP, bool GATE>

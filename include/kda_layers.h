@@ -13,6 +13,9 @@
  * Token axis: dense batches are [B, T, ...]; packed sequences have B = 1, T tokens in all and
  * cu_seqlens (device and host copies with the same values) with N sequences, empty ones allowed.
  *
+ * Outputs and the workspace overlap neither each other nor an input; `state` of a token step is the
+ * only argument that is read and written.
+ *
  * Rows: tensors are contiguous, except that an input named with a *_row field may be a column
  * slice of a wider contiguous matrix: its element (token i, column c) is at i * row + c, tokens
  * counted over the whole batch. A row of 0 means the tensor's own width.
