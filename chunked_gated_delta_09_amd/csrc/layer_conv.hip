@@ -65,8 +65,8 @@ __device__ __forceinline__ void history_row(const ConvArgs& a, int n, int64_t be
   }
 }
 
-// The filters of VEC channels, VEC * W numbers in a row: 16 bytes a load where VEC > 1 (all channels
-// exist then) and the array is aligned.
+// The filters of VEC channels, VEC * W numbers in a row: 16 bytes a load where they are whole pieces of
+// that and the array is aligned.
 template <int W, int VEC>
 __device__ __forceinline__ void load_filter(const float* weight, const float* bias, int wvec, int ch, float (&w)[W][VEC],
                                             float (&b)[VEC]) {
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t run_b
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const float u = tap_sum<W, VEC>(w, win, b[e], e);
-          const float du = g[e] * (a.act ? dact_f(u, KDA_ACT_SILU) : 1.f);
+          const float du = g[e] * (a.act ? dsilu(u) : 1.f);
 #pragma unroll
           for (int j = 0; j < W; ++j)
             if (t + j < W - 1) acc[t + j][e] = fmaf(w[j][e], du, acc[t + j][e]);
@@ -279,7 +279,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t run_b
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float u = tap_sum<W, VEC>(w, win, b[e], e);
-        const float du = gin.at(e) * (a.act ? dact_f(u, KDA_ACT_SILU) : 1.f);
+        const float du = gin.at(e) * (a.act ? dsilu(u) : 1.f);
 #pragma unroll
         for (int j = 0; j < W; ++j)
           if (j >= from) pend[j][e] = fmaf(w[j][e], du, pend[j][e]);

@@ -53,8 +53,8 @@ __device__ __forceinline__ Pack<T, N> load_n(const T* p, int valid, bool vec) {
   return r;
 }
 
-// N values to p, rounded to T; those from `valid` on are left. The 16-byte and the single stores take
-// different words, or the compiler joins the two ways into one of single stores.
+// N values to p, rounded to T; those from `valid` on are left. The wide and the single stores take different
+// words, or the compiler joins the two ways into one of single stores.
 template <class T, int N>
 __device__ __forceinline__ void store_n(T* p, const float (&x)[N], int valid, bool vec) {
   if (vec && valid >= N && N > 1) {
@@ -111,16 +111,10 @@ __device__ __forceinline__ float softplus(float x) {
   return fmaf(__builtin_amdgcn_logf(u), kLn2, fmaf(e - (u - 1.f), __builtin_amdgcn_rcpf(u), top));
 }
 
-// y = act(x) and its derivative for kda_act codes.
-__device__ __forceinline__ float act_f(float x, int act) {
-  if (act == KDA_ACT_NONE) return x;
+// The derivative of x sigmoid(x).
+__device__ __forceinline__ float dsilu(float x) {
   const float s = sigmoid(x);
-  return act == KDA_ACT_SIGMOID ? s : x * s;
-}
-__device__ __forceinline__ float dact_f(float x, int act) {
-  if (act == KDA_ACT_NONE) return 1.f;
-  const float s = sigmoid(x);
-  return act == KDA_ACT_SIGMOID ? s * (1.f - s) : s * (1.f + x * (1.f - s));
+  return s * (1.f + x * (1.f - s));
 }
 
 // Moves within rows of 16 lanes (DPP controls): quad permutations, mirrors, rotations, shifts.

@@ -160,10 +160,11 @@ template <class T, int NP>
 struct Stage {
   typedef Lanes<NP> L;
   int tid, per, grp, c0;
-  bool inner;  // all channels of the tile exist, four-element loads are aligned
+  bool vec;    // four-element loads are aligned; a piece's channels then exist all or none
+  bool inner;  // and all channels of the tile exist
 
   __device__ __forceinline__ Stage(const ScanArgs& a, int grp_, int c0_)
-      : tid(threadIdx.x), per(a.D / a.G), grp(grp_), c0(c0_), inner(a.vec != 0 && c0_ + L::CH <= a.D / a.G) {}
+      : tid(threadIdx.x), per(a.D / a.G), grp(grp_), c0(c0_), vec(a.vec != 0), inner(vec && c0_ + L::CH <= a.D / a.G) {}
   // To be called once a chunk: what follows from the thread's number (places, masks, the addresses of
   // partial chunks) is formed again rather than kept in registers across the recurrence.
   __device__ __forceinline__ void renew() { asm volatile("" : "+v"(tid)); }
@@ -187,7 +188,12 @@ struct Stage {
       if (has(k)) return load_n<T, 4>(q, 4, true);
       return Pack<T, 4>{};
     }
-    return load_n<T, 4>(q, has(k) && token(k) < live ? per - c0 - col(k) : 0, inner);
+    const int valid = has(k) && token(k) < live ? per - c0 - col(k) : 0;
+    if (vec) {
+      if (valid > 0) return load_n<T, 4>(q, 4, true);
+      return Pack<T, 4>{};
+    }
+    return load_n<T, 4>(q, valid, false);
   }
   __device__ __forceinline__ T load_bc(const void* p, int64_t t, int64_t row, uint32_t off, int k, int N, int live) const {
     const T* q = reinterpret_cast<const T*>(static_cast<const char*>(p) + t * row * (int64_t)sizeof(T) + off);
@@ -196,7 +202,12 @@ struct Stage {
   __device__ __forceinline__ void store(void* p, int64_t t, int64_t row, uint32_t off, int k, int live,
                                         const float (&v)[4]) const {
     T* q = reinterpret_cast<T*>(static_cast<char*>(p) + t * row * (int64_t)sizeof(T) + off);
-    if (has(k) && token(k) < live) store_n<T, 4>(q, v, inner ? 4 : per - c0 - col(k), inner);
+    const int valid = has(k) && token(k) < live ? per - c0 - col(k) : 0;
+    if (vec) {
+      if (valid > 0) store_n<T, 4>(q, v, 4, true);
+    } else {
+      store_n<T, 4>(q, v, valid, false);
+    }
   }
   // a parameter of the tile's channels to shared memory
   __device__ __forceinline__ void params(const float* p, float* to) const {
