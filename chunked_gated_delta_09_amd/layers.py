@@ -173,18 +173,33 @@ def _cuts(cu_seqlens, cu_seqlens_dev, B, dev):
     return len(cu) - 1, ptr, (_i32 * len(cu))(*cu), cu_seqlens_dev
 
 
-# The size structures of calls without cuts, by their values: the library only reads them.
-@functools.lru_cache(maxsize=512)
-def _dims(kind, *values):
-    d = kind(*values)
-    return d, ctypes.byref(d)
+class _Plan:
+    """A size structure, the reference that calls take, and the sizes that the library has answered for it."""
+
+    __slots__ = ("dims", "ref", "sizes")
+
+    def __init__(self, kind, *values):
+        self.dims = kind(*values)
+        self.ref = ctypes.byref(self.dims)
+        self.sizes = {}
+
+    def size(self, query):
+        n = self.sizes.get(query)
+        if n is None:
+            n = getattr(_lib(), query)(self.ref)
+            if n > 0:
+                self.sizes[query] = n
+        return n
 
 
-def _dims_of(kind, cu_dev, cu_host, before, after):
+# Those of calls without cuts are kept, by their values alone: the library only reads them.
+_plan = functools.lru_cache(maxsize=512)(_Plan)
+
+
+def _plan_of(kind, cu_dev, cu_host, before, after):
     if cu_host is None:
-        return _dims(kind, *before, None, None, *after)
-    d = kind(*before, cu_dev, cu_host, *after)
-    return d, ctypes.byref(d)
+        return _plan(kind, *before, None, None, *after)
+    return _Plan(kind, *before, cu_dev, cu_host, *after)
 
 
 @functools.lru_cache(maxsize=512)
@@ -203,21 +218,27 @@ def _ws(like, n):
     """A workspace of n bytes and its address."""
     if not n:
         return None, None
-    ws = torch.empty(n, dtype=torch.uint8, device=like.device)
+    ws = like.new_empty(n, dtype=torch.uint8)
     return ws, ws.data_ptr()
 
 
 def _new(like, shape, dtype=None):
-    """A contiguous tensor of this shape, of the type (but for `dtype`) and on the GPU of `like`, and its address."""
-    if dtype is None and like.shape == shape and like.is_contiguous():
-        t = torch.empty_like(like)
-    else:
-        t = like.new_empty(shape, dtype=dtype)
+    """A tensor of this shape, of the type (but for `dtype`) and on the GPU of `like`, and its address."""
+    t = like.new_empty(shape, dtype=dtype)
     return t, t.data_ptr()
 
 
 def _new_if(cond, like, shape, dtype=None):
     return _new(like, shape, dtype) if cond else (None, None)
+
+
+def _like(t, row=0):
+    """A contiguous tensor of the shape, type and GPU of `t`, and its address. `row`: what _rows found for `t`
+    (0: `t` is contiguous itself, and empty_like, the cheapest call, lays the new one out the same)."""
+    if t is None:
+        return None, None
+    r = t.new_empty(t.shape) if row else torch.empty_like(t)
+    return r, r.data_ptr()
 
 
 F32 = torch.float32
@@ -236,8 +257,8 @@ def _conv(x, weight, bias, h0, cu_seqlens, cu_seqlens_dev, activation):
     px, row = _rows(x, "x", x.dtype, (B, T, D), dev, 2)
     ptrs = (px, _need(weight, "weight", F32, (D, W), dev), _need(bias, "bias", F32, (D,), dev),
             _need(h0, "h0", x.dtype, (N, W - 1, D), dev))
-    d = _dims_of(_ConvDims, cu_dev, cu_host, (B, T, D, W, N), (row, _act(activation, (None, "silu")), _DT[x.dtype]))
-    return d[1], dev, (B, T, D, W, N), ptrs, (d, keep)
+    plan = _plan_of(_ConvDims, cu_dev, cu_host, (B, T, D, W, N), (row, _act(activation, (None, "silu")), _DT[x.dtype]))
+    return plan, dev, (B, T, D, W, N), row, ptrs, keep
 
 
 def short_conv(x, weight, bias=None, h0=None, cu_seqlens=None, cu_seqlens_dev=None, activation="silu",
@@ -246,10 +267,10 @@ def short_conv(x, weight, bias=None, h0=None, cu_seqlens=None, cu_seqlens_dev=No
     x_{t-(W-1)+j}, y = u or silu(u). x [B,T,D]; weight [D,W] fp32 (W = 2, 3, 4; the last tap sees the
     current token); bias [D] fp32; h0 [N,W-1,D]: the rows before each sequence's first. Returns
     dict(y [B,T,D], final_state [N,W-1,D] or None: the last W-1 rows of [h0 | x])."""
-    d, dev, (B, T, D, W, N), ptrs, keep = _conv(x, weight, bias, h0, cu_seqlens, cu_seqlens_dev, activation)
-    y, py = _new(x, (B, T, D))
+    plan, dev, (B, T, D, W, N), row, ptrs, keep = _conv(x, weight, bias, h0, cu_seqlens, cu_seqlens_dev, activation)
+    y, py = _like(x, row)
     final, pf = _new_if(output_final_state, x, (N, W - 1, D))
-    _launch(dev, _lib().kda_short_conv_fwd, d, *ptrs, py, pf)
+    _launch(dev, _lib().kda_short_conv_fwd, plan.ref, *ptrs, py, pf)
     del keep
     return dict(y=y, final_state=final)
 
@@ -258,17 +279,13 @@ def short_conv_bwd(x, weight, dy, bias=None, h0=None, dfinal=None, cu_seqlens=No
                    activation="silu"):
     """Gradients of sum<dy, y> + <dfinal, final_state>. Returns dict(dx [B,T,D], dweight [D,W] fp32,
     dbias [D] fp32 or None, dh0 [N,W-1,D] or None)."""
-    d, dev, (B, T, D, W, N), ptrs, keep = _conv(x, weight, bias, h0, cu_seqlens, cu_seqlens_dev, activation)
+    plan, dev, (B, T, D, W, N), row, ptrs, keep = _conv(x, weight, bias, h0, cu_seqlens, cu_seqlens_dev, activation)
     pdy = _need(dy, "dy", x.dtype, (B, T, D), dev)
     pdf = _need(dfinal, "dfinal", x.dtype, (N, W - 1, D), dev)
-    lib = _lib()
-    need = lib.kda_short_conv_bwd_workspace_bytes(d)
-    dx, pdx = _new(x, (B, T, D))
-    dw, pdw = _new(x, (D, W), F32)
-    db, pdb = _new_if(bias is not None, x, (D,), F32)
-    dh0, pdh0 = _new_if(h0 is not None, x, (N, W - 1, D))
+    need = plan.size("kda_short_conv_bwd_workspace_bytes")
+    (dx, pdx), (dw, pdw), (db, pdb), (dh0, pdh0) = _like(x, row), _like(weight), _like(bias), _like(h0)
     ws, pws = _ws(x, need)
-    _launch(dev, lib.kda_short_conv_bwd, d, *ptrs, pdy, pdf, pdx, pdw, pdb, pdh0, pws, need)
+    _launch(dev, _lib().kda_short_conv_bwd, plan.ref, *ptrs, pdy, pdf, pdx, pdw, pdb, pdh0, pws, need)
     del keep
     return dict(dx=dx, dweight=dw, dbias=db, dh0=dh0)
 
@@ -285,9 +302,9 @@ def short_conv_step(x, state, weight, bias=None, slots=None, activation="silu"):
     pb = _need(bias, "bias", F32, (D,), dev)
     pst = _need(state, "state", x.dtype, (S, W - 1, D), dev)
     psl = _need(slots, "slots", torch.int32, (B,), dev)
-    _, d = _dims(_ConvDims, B, 1, D, W, B, None, None, row, _act(activation, (None, "silu")), _DT[x.dtype])
-    y, py = _new(x, (B, D))
-    _launch(dev, _lib().kda_short_conv_step, d, px, pw, pb, psl, S, pst, py)
+    plan = _plan(_ConvDims, B, 1, D, W, B, None, None, row, _act(activation, (None, "silu")), _DT[x.dtype])
+    y, py = _like(x, row)
+    _launch(dev, _lib().kda_short_conv_step, plan.ref, px, pw, pb, psl, S, pst, py)
     return y
 
 
@@ -310,9 +327,10 @@ def _scan(x, dt, A, B, C, skip, z, dt_bias, softplus, lead, cuts):
     pC, rC = _rows(C, "C", dt_, bc, dev, lead)
     ptrs = (px, pdt, _need(A, "A", F32, (D, NS), dev), pB, pC, _need(skip, "skip", F32, (D,), dev), pz,
             _need(dt_bias, "dt_bias", F32, (D,), dev))
-    d = _dims_of(_ScanDims, cu_dev, cu_host, (rows[0], rows[1] if lead == 2 else 1, D, NS, G, N),
-                 (rx, rdt, rz, rB, rC, int(bool(softplus)), _DT[dt_]))
-    return d[1], dev, (rows, D, NS, G, N), ptrs, (d, keep)
+    strides = (rx, rdt, rz, rB, rC)
+    plan = _plan_of(_ScanDims, cu_dev, cu_host, (rows[0], rows[1] if lead == 2 else 1, D, NS, G, N),
+                    strides + (int(bool(softplus)), _DT[dt_]))
+    return plan, dev, (rows, D, NS, N), strides, ptrs, keep
 
 
 def selective_scan(x, dt, A, B, C, skip=None, z=None, dt_bias=None, h0=None, cu_seqlens=None, cu_seqlens_dev=None,
@@ -322,19 +340,18 @@ def selective_scan(x, dt, A, B, C, skip=None, z=None, dt_bias=None, h0=None, cu_
     [B,T,G,NS], shared by the D/G channels of a group; skip, dt_bias [D] fp32; h0 [N,D,NS] fp32.
     Returns dict(y [B,T,D], final_state [N,D,NS] fp32 or None, states or None). ``save``: keep the state
     entering every SCAN_CHUNK tokens (fp32 [chunks,D,NS]) for ``selective_scan_bwd``."""
-    d, dev, (rows, D, NS, G, N), ptrs, keep = _scan(x, dt, A, B, C, skip, z, dt_bias, dt_softplus, 2,
-                                                    (cu_seqlens, cu_seqlens_dev))
+    plan, dev, (rows, D, NS, N), strides, ptrs, keep = _scan(x, dt, A, B, C, skip, z, dt_bias, dt_softplus, 2,
+                                                             (cu_seqlens, cu_seqlens_dev))
     ph0 = _need(h0, "h0", F32, (N, D, NS), dev)
-    lib = _lib()
-    chunks = lib.kda_sscan_num_chunks(d)
+    chunks = plan.size("kda_sscan_num_chunks")
     if chunks < 0:
-        raise KdaError(-1, lib.kda_last_error().decode())
-    need = lib.kda_sscan_fwd_workspace_bytes(d)
-    y, py = _new(x, rows + (D,))
+        raise KdaError(-1, _lib().kda_last_error().decode())
+    need = plan.size("kda_sscan_fwd_workspace_bytes")
+    y, py = _like(x, strides[0])
     final, pf = _new_if(output_final_state, x, (N, D, NS), F32)
     states, ps = _new_if(save, x, (chunks, D, NS), F32)
     ws, pws = _ws(x, need)
-    _launch(dev, lib.kda_sscan_fwd, d, *ptrs, ph0, py, pf, ps, pws, need)
+    _launch(dev, _lib().kda_sscan_fwd, plan.ref, *ptrs, ph0, py, pf, ps, pws, need)
     del keep
     return dict(y=y, final_state=final, states=states)
 
@@ -345,25 +362,23 @@ def selective_scan_bwd(x, dt, A, B, C, states, dy, skip=None, z=None, dt_bias=No
     ``selective_scan(..., save=True)`` on the same arguments. Returns dict(dx, ddt [B,T,D], dA [D,NS]
     fp32, dB, dC [B,T,G,NS], dskip [D] fp32 or None, dz [B,T,D] or None, ddt_bias [D] fp32 or None, dh0
     [N,D,NS] fp32 or None)."""
-    d, dev, (rows, D, NS, G, N), ptrs, keep = _scan(x, dt, A, B, C, skip, z, dt_bias, dt_softplus, 2,
-                                                    (cu_seqlens, cu_seqlens_dev))
-    lib = _lib()
-    chunks = lib.kda_sscan_num_chunks(d)
+    plan, dev, (rows, D, NS, N), strides, ptrs, keep = _scan(x, dt, A, B, C, skip, z, dt_bias, dt_softplus, 2,
+                                                             (cu_seqlens, cu_seqlens_dev))
+    chunks = plan.size("kda_sscan_num_chunks")
     if chunks < 0:
-        raise KdaError(-1, lib.kda_last_error().decode())
+        raise KdaError(-1, _lib().kda_last_error().decode())
     pst = _need(states, "states", F32, (chunks, D, NS), dev)
-    pdy = _need(dy, "dy", x.dtype, rows + (D,), dev)
+    pdy = _need(dy, "dy", x.dtype, x.shape, dev)
     pdf = _need(dfinal, "dfinal", F32, (N, D, NS), dev)
-    need = _bytes(lib.kda_sscan_bwd_workspace_bytes(d))
-    wide, bc = rows + (D,), rows + (G, NS)
-    (dx, pdx), (ddt, pddt), (dA, pdA) = _new(x, wide), _new(x, wide), _new(x, (D, NS), F32)
-    (dB, pdB), (dC, pdC) = _new(x, bc), _new(x, bc)
-    dskip, pds = _new_if(skip is not None, x, (D,), F32)
-    dz, pdz = _new_if(z is not None, x, wide)
-    dbias, pdb = _new_if(dt_bias is not None, x, (D,), F32)
+    need = _bytes(plan.size("kda_sscan_bwd_workspace_bytes"))
+    rx, rdt, rz, rB, rC = strides
+    (dx, pdx), (ddt, pddt), (dz, pdz) = _like(x, rx), _like(dt, rdt), _like(z, rz)
+    (dB, pdB), (dC, pdC) = _like(B, rB), _like(C, rC)
+    (dA, pdA), (dskip, pds), (dbias, pdb) = _like(A), _like(skip), _like(dt_bias)
     dh0, pdh0 = _new_if(output_dh0, x, (N, D, NS), F32)
     ws, pws = _ws(x, need)
-    _launch(dev, lib.kda_sscan_bwd, d, *ptrs, pst, pdy, pdf, pdx, pddt, pdA, pdB, pdC, pds, pdz, pdb, pdh0, pws, need)
+    _launch(dev, _lib().kda_sscan_bwd, plan.ref, *ptrs, pst, pdy, pdf, pdx, pddt, pdA, pdB, pdC, pds, pdz, pdb, pdh0,
+            pws, need)
     del keep
     return dict(dx=dx, ddt=ddt, dA=dA, dB=dB, dC=dC, dskip=dskip, dz=dz, ddt_bias=dbias, dh0=dh0)
 
@@ -371,15 +386,14 @@ def selective_scan_bwd(x, dt, A, B, C, states, dy, skip=None, z=None, dt_bias=No
 def selective_scan_step(x, dt, A, B, C, state, slots=None, skip=None, z=None, dt_bias=None, dt_softplus=False):
     """One token of each sequence: x, dt, z [B,D], B, C [B,G,NS], state [S,D,NS] fp32 updated in place.
     Returns y [B,D]."""
-    d, dev, (rows, D, NS, G, N), ptrs, keep = _scan(x, dt, A, B, C, skip, z, dt_bias, dt_softplus, 1, (None, None))
+    plan, dev, (rows, D, NS, _), strides, ptrs, _ = _scan(x, dt, A, B, C, skip, z, dt_bias, dt_softplus, 1, (None, None))
     if state.dim() != 3:
         raise ValueError("state must be [S, D, NS]")
     S = state.shape[0]
     pst = _need(state, "state", F32, (S, D, NS), dev)
     psl = _need(slots, "slots", torch.int32, rows, dev)
-    y, py = _new(x, rows + (D,))
-    _launch(dev, _lib().kda_sscan_step, d, *ptrs, psl, S, pst, py)
-    del keep
+    y, py = _like(x, strides[0])
+    _launch(dev, _lib().kda_sscan_step, plan.ref, *ptrs, psl, S, pst, py)
     return y
 
 
@@ -399,9 +413,9 @@ def _norm(x, groups, weight, bias, gate, activation, center, eps):
     shared = first is not None and groups > 1 and first.dim() == 1 and first.shape[0] == C
     n = (C if shared else W,)
     ptrs = (px, _need(weight, "weight", F32, n, dev), _need(bias, "bias", F32, n, dev), pg)
-    _, d = _dims(_NormDims, x.numel() // W, groups, C, int(bool(center)), _act(activation, (None, "silu", "sigmoid")),
+    plan = _plan(_NormDims, x.numel() // W, groups, C, int(bool(center)), _act(activation, (None, "silu", "sigmoid")),
                  int(shared), float(eps), x_row, gate_row, _DT[x.dtype])
-    return d, dev, ptrs
+    return plan, dev, (x_row, gate_row), ptrs
 
 
 def group_norm(x, groups, weight=None, bias=None, gate=None, activation=None, center=False, eps=1e-5):
@@ -409,24 +423,20 @@ def group_norm(x, groups, weight=None, bias=None, gate=None, activation=None, ce
     ``center``, (x - mean) / std), u = n weight + bias, y = act(u), or u act(gate) with a gate of x's
     shape. weight and bias fp32, [groups*C] or [C] (one for all groups). activation: None, "silu",
     "sigmoid". Returns y."""
-    d, dev, ptrs = _norm(x, groups, weight, bias, gate, activation, center, eps)
-    y, py = _new(x, x.shape)
-    _launch(dev, _lib().kda_group_norm_fwd, d, *ptrs, py)
+    plan, dev, (x_row, _), ptrs = _norm(x, groups, weight, bias, gate, activation, center, eps)
+    y, py = _like(x, x_row)
+    _launch(dev, _lib().kda_group_norm_fwd, plan.ref, *ptrs, py)
     return y
 
 
 def group_norm_bwd(x, groups, dy, weight=None, bias=None, gate=None, activation=None, center=False, eps=1e-5):
     """Gradients of sum<dy, y>. Returns dict(dx, dweight, dbias, dgate), None where the input is."""
-    d, dev, ptrs = _norm(x, groups, weight, bias, gate, activation, center, eps)
+    plan, dev, (x_row, gate_row), ptrs = _norm(x, groups, weight, bias, gate, activation, center, eps)
     pdy = _need(dy, "dy", x.dtype, x.shape, dev)
-    lib = _lib()
-    need = lib.kda_group_norm_bwd_workspace_bytes(d) if weight is not None or bias is not None else 0
-    dx, pdx = _new(x, x.shape)
-    dw, pdw = _new_if(weight is not None, x, weight.shape if weight is not None else None, F32)
-    db, pdb = _new_if(bias is not None, x, bias.shape if bias is not None else None, F32)
-    dgate, pdg = _new_if(gate is not None, x, x.shape)
+    need = plan.size("kda_group_norm_bwd_workspace_bytes") if weight is not None or bias is not None else 0
+    (dx, pdx), (dw, pdw), (db, pdb), (dgate, pdg) = _like(x, x_row), _like(weight), _like(bias), _like(gate, gate_row)
     ws, pws = _ws(x, need)
-    _launch(dev, lib.kda_group_norm_bwd, d, *ptrs, pdy, pdx, pdw, pdb, pdg, pws, need)
+    _launch(dev, _lib().kda_group_norm_bwd, plan.ref, *ptrs, pdy, pdx, pdw, pdb, pdg, pws, need)
     return dict(dx=dx, dweight=dw, dbias=db, dgate=dgate)
 
 
@@ -446,6 +456,6 @@ def kda_step(q, k, v, g, beta, state, slots=None, scale=None, beta_logits=False)
             _need(slots, "slots", torch.int32, (B,), dev))
     pst = _need(state, "state", F32, (S, HV, K, V), dev)
     _, d = _kda_dims(B, H, HV, K, V, scale, "f32" if dt is F32 else "bf16", bool(beta_logits))
-    o, po = _new(v, (B, HV, V))
+    o, po = _like(v)
     _launch(dev, _lib().kda_step, d, *ptrs, S, pst, po)
     return o
