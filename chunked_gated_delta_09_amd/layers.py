@@ -386,7 +386,8 @@ def selective_scan_bwd(x, dt, A, B, C, states, dy, skip=None, z=None, dt_bias=No
 def selective_scan_step(x, dt, A, B, C, state, slots=None, skip=None, z=None, dt_bias=None, dt_softplus=False):
     """One token of each sequence: x, dt, z [B,D], B, C [B,G,NS], state [S,D,NS] fp32 updated in place.
     Returns y [B,D]."""
-    plan, dev, (rows, D, NS, _), strides, ptrs, _ = _scan(x, dt, A, B, C, skip, z, dt_bias, dt_softplus, 1, (None, None))
+    plan, dev, (rows, D, NS, _), strides, ptrs, _ = _scan(x, dt, A, B, C, skip, z, dt_bias, dt_softplus, 1,
+                                                          (None, None))
     if state.dim() != 3:
         raise ValueError("state must be [S, D, NS]")
     S = state.shape[0]
