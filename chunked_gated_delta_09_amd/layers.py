@@ -456,6 +456,8 @@ def kda_step(q, k, v, g, beta, state, slots=None, scale=None, beta_logits=False)
             _need(g, "g", F32, (B, HV, K), dev), _need(beta, "beta", F32, (B, HV), dev),
             _need(slots, "slots", torch.int32, (B,), dev))
     pst = _need(state, "state", F32, (S, HV, K, V), dev)
+    # by value: a tensor as a key would stand for whatever it held at the first call
+    scale = None if scale is None else float(scale)
     _, d = _kda_dims(B, H, HV, K, V, scale, "f32" if dt is F32 else "bf16", bool(beta_logits))
     o, po = _like(v)
     _launch(dev, _lib().kda_step, d, *ptrs, S, pst, po)
