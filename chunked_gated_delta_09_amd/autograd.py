@@ -60,11 +60,19 @@ def kda_chunk(q, k, v, g, beta, h0=None, cu_seqlens=None, C=64, scale=None, outp
                                   save_operands)
 
 
+def _kept(cu_seqlens):
+    """The cuts as they are now: the backward may run after the caller has refilled their list or buffer."""
+    if cu_seqlens is None:
+        return None
+    return tuple(int(c) for c in (cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens))
+
+
 class ShortConvFunction(torch.autograd.Function):
     """y, final_state = short_conv(x, weight, bias, h0) with gradients for all four."""
 
     @staticmethod
     def forward(ctx, x, weight, bias, h0, cu_seqlens, cu_seqlens_dev, activation, output_final_state):
+        cu_seqlens = _kept(cu_seqlens)
         f = layers.short_conv(x, weight, bias=bias, h0=h0, cu_seqlens=cu_seqlens, cu_seqlens_dev=cu_seqlens_dev,
                               activation=activation, output_final_state=output_final_state)
         ctx.save_for_backward(x, weight, bias, h0, cu_seqlens_dev)
@@ -93,6 +101,7 @@ class SelectiveScanFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, dt, A, B, C, skip, z, dt_bias, h0, cu_seqlens, cu_seqlens_dev, dt_softplus, output_final_state):
+        cu_seqlens = _kept(cu_seqlens)
         f = layers.selective_scan(x, dt, A, B, C, skip=skip, z=z, dt_bias=dt_bias, h0=h0, cu_seqlens=cu_seqlens,
                                   cu_seqlens_dev=cu_seqlens_dev, dt_softplus=dt_softplus,
                                   output_final_state=output_final_state, save=True)

@@ -1,0 +1,60 @@
+"""The autograd wrappers without a GPU: what they keep between the forward and the backward, seen at the calls that they
+make of the binding (stand-ins on the CPU here)."""
+import numpy as np
+import pytest
+import torch
+
+from chunked_gated_delta_09_amd import autograd as ag
+
+CUTS = [0, 2, 5]
+
+
+def record(monkeypatch, module, names, results):
+    """Puts stand-ins for a forward and a backward in place; returns the list of the keyword arguments they were called
+    with, cuts copied as they stood."""
+    calls = []
+
+    def stand_in(result):
+        def call(*args, **kw):
+            cu = kw.get("cu_seqlens")
+            calls.append(dict(kw, cu_seqlens=None if cu is None else [int(c) for c in cu]))
+            return {k: v() for k, v in result.items()}
+        return call
+
+    for name, result in zip(names, results):
+        monkeypatch.setattr(module, name, stand_in(result))
+    return calls
+
+
+def refill(cu, values):
+    for i, v in enumerate(values):
+        cu[i] = v
+
+
+def zeros(*shape):
+    return lambda: torch.zeros(*shape)
+
+
+@pytest.mark.parametrize("kind", [list, np.array, torch.tensor], ids=["list", "numpy", "tensor"])
+def test_short_conv_keeps_its_cuts(monkeypatch, kind):
+    calls = record(monkeypatch, ag.layers, ("short_conv", "short_conv_bwd"),
+                   (dict(y=zeros(1, 5, 3), final_state=lambda: None),
+                    dict(dx=zeros(1, 5, 3), dweight=zeros(3, 4), dbias=lambda: None, dh0=lambda: None)))
+    x, w, cu = torch.zeros(1, 5, 3, requires_grad=True), torch.zeros(3, 4), kind(CUTS)
+    y, _ = ag.short_conv(x, w, cu_seqlens=cu)
+    refill(cu, [0, 4, 5])  # the caller's buffer holds the next batch's cuts by the time of the backward
+    y.sum().backward()
+    assert [c["cu_seqlens"] for c in calls] == [CUTS, CUTS]
+
+
+@pytest.mark.parametrize("kind", [list, np.array, torch.tensor], ids=["list", "numpy", "tensor"])
+def test_selective_scan_keeps_its_cuts(monkeypatch, kind):
+    none = dict(dskip=lambda: None, dz=lambda: None, ddt_bias=lambda: None, dh0=lambda: None)
+    calls = record(monkeypatch, ag.layers, ("selective_scan", "selective_scan_bwd"),
+                   (dict(y=zeros(1, 5, 3), final_state=lambda: None, states=zeros(3, 3, 2)),
+                    dict(dx=zeros(1, 5, 3), ddt=zeros(1, 5, 3), dA=zeros(3, 2), dB=zeros(1, 5, 1, 2), dC=zeros(1, 5, 1, 2), **none)))
+    x, A, B, cu = torch.zeros(1, 5, 3, requires_grad=True), torch.zeros(3, 2), torch.zeros(1, 5, 1, 2), kind(CUTS)
+    y, _ = ag.selective_scan(x, x.detach(), A, B, B, cu_seqlens=cu, output_final_state=False)
+    refill(cu, [0, 4, 5])
+    y.sum().backward()
+    assert [c["cu_seqlens"] for c in calls] == [CUTS, CUTS]
