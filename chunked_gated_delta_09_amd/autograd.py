@@ -136,7 +136,7 @@ class GroupNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, gate, groups, activation, center, eps):
         ctx.save_for_backward(x, weight, bias, gate)
-        ctx.args = dict(activation=activation, center=center, eps=eps)
+        ctx.args = dict(activation=activation, center=center, eps=float(eps))
         ctx.groups = groups
         return layers.group_norm(x, groups, weight=weight, bias=bias, gate=gate, **ctx.args)
 

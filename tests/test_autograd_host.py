@@ -58,3 +58,15 @@ def test_selective_scan_keeps_its_cuts(monkeypatch, kind):
     refill(cu, [0, 4, 5])
     y.sum().backward()
     assert [c["cu_seqlens"] for c in calls] == [CUTS, CUTS]
+
+
+def test_group_norm_keeps_its_eps(monkeypatch):
+    seen = []
+    monkeypatch.setattr(ag.layers, "group_norm", lambda x, groups, eps, **kw: seen.append(float(eps)) or torch.zeros_like(x))
+    monkeypatch.setattr(ag.layers, "group_norm_bwd", lambda x, groups, dy, eps, **kw: seen.append(float(eps)) or dict(
+        dx=torch.zeros_like(x), dweight=None, dbias=None, dgate=None))
+    eps = torch.tensor(0.5)
+    y = ag.group_norm(torch.zeros(2, 4, requires_grad=True), 2, eps=eps)
+    eps.fill_(2.0)
+    y.sum().backward()
+    assert seen == [0.5, 0.5]
