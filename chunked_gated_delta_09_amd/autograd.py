@@ -21,6 +21,13 @@ from torch.autograd.function import once_differentiable
 from . import chunk_bwd, fwd_states, layers
 
 
+def _kept(cu_seqlens):
+    """The cuts as they are now: the backward may run after the caller has refilled their list or buffer."""
+    if cu_seqlens is None:
+        return None
+    return tuple(int(c) for c in (cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens))
+
+
 class KdaChunkFunction(torch.autograd.Function):
     """o, S_T = KDA(q, k, v, g, beta, h0) with gradients for q, k, v, g, beta and h0.
 
@@ -30,6 +37,7 @@ class KdaChunkFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, g, beta, h0, cu_seqlens, C, scale, output_final_state, beta_logits, save_operands):
+        cu_seqlens, scale = _kept(cu_seqlens), None if scale is None else float(scale)
         fw = fwd_states(q, k, v, g, beta, h0=h0, cu_seqlens=cu_seqlens, C=C, scale=scale, output_o=True,
                         output_final_state=output_final_state, beta_logits=beta_logits, save=save_operands)
         ctx.save_for_backward(q, k, v, g, beta, fw["states"], fw["inv"], fw["saved"])
@@ -58,13 +66,6 @@ def kda_chunk(q, k, v, g, beta, h0=None, cu_seqlens=None, C=64, scale=None, outp
     [N,HV,K,V] fp32 or None)."""
     return KdaChunkFunction.apply(q, k, v, g, beta, h0, cu_seqlens, C, scale, output_final_state, beta_logits,
                                   save_operands)
-
-
-def _kept(cu_seqlens):
-    """The cuts as they are now: the backward may run after the caller has refilled their list or buffer."""
-    if cu_seqlens is None:
-        return None
-    return tuple(int(c) for c in (cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens))
 
 
 class ShortConvFunction(torch.autograd.Function):

@@ -70,3 +70,18 @@ def test_group_norm_keeps_its_eps(monkeypatch):
     eps.fill_(2.0)
     y.sum().backward()
     assert seen == [0.5, 0.5]
+
+
+@pytest.mark.parametrize("kind", [list, np.array, torch.tensor], ids=["list", "numpy", "tensor"])
+def test_kda_chunk_keeps_its_cuts_and_scale(monkeypatch, kind):
+    one = zeros(1, 5, 1, 2)
+    calls = record(monkeypatch, ag, ("fwd_states", "chunk_bwd"),
+                   (dict(o=one, final_state=lambda: None, states=one, inv=one, saved=one),
+                    dict(dq=one, dk=one, dv=one, dg=one, dbeta=zeros(1, 5, 1))))
+    q, beta, cu, scale = one().requires_grad_(), torch.zeros(1, 5, 1), kind(CUTS), torch.tensor(0.5)
+    o, _ = ag.kda_chunk(q, one(), one(), one(), beta, cu_seqlens=cu, scale=scale, output_final_state=False)
+    refill(cu, [0, 4, 5])
+    scale.fill_(2.0)
+    o.sum().backward()
+    assert [c["cu_seqlens"] for c in calls] == [CUTS, CUTS]
+    assert [float(c["scale"]) for c in calls] == [0.5, 0.5]
