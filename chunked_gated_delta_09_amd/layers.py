@@ -15,6 +15,9 @@ Token steps update the state in place. ``slots`` (int32 [B] on the GPU) names th
 batch row; None: row b. A negative slot marks a padding row (no state is touched, its output is
 zero); a slot behind the state's last row, or one that an earlier batch row has as well, is refused
 on the GPU: no state is touched for that row and its output is NaN.
+
+Nothing here is recorded by autograd (``autograd`` has the differentiable forms). A state that a graph has
+saved for its backward is too new for it after a step, as after any in-place operation.
 """
 from __future__ import annotations
 
@@ -91,6 +94,13 @@ def _launch(dev, fn, *args):
             status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status:
         _check(status)
+
+
+def _step(dev, fn, state, *args):
+    """_launch for a call that writes `state`. Torch does not see a write through an address: the tensor's version is
+    counted up by hand, so that a graph which has saved it refuses its backward."""
+    _launch(dev, fn, *args)
+    torch._C._increment_version((state,))
 
 
 def _refuse(t, name, dtype, shape, dev):
@@ -304,7 +314,7 @@ def short_conv_step(x, state, weight, bias=None, slots=None, activation="silu"):
     psl = _need(slots, "slots", torch.int32, (B,), dev)
     plan = _plan(_ConvDims, B, 1, D, W, B, None, None, row, _act(activation, (None, "silu")), _DT[x.dtype])
     y, py = _like(x, row)
-    _launch(dev, _lib().kda_short_conv_step, plan.ref, px, pw, pb, psl, S, pst, py)
+    _step(dev, _lib().kda_short_conv_step, state, plan.ref, px, pw, pb, psl, S, pst, py)
     return y
 
 
@@ -394,7 +404,7 @@ def selective_scan_step(x, dt, A, B, C, state, slots=None, skip=None, z=None, dt
     pst = _need(state, "state", F32, (S, D, NS), dev)
     psl = _need(slots, "slots", torch.int32, rows, dev)
     y, py = _like(x, strides[0])
-    _launch(dev, _lib().kda_sscan_step, plan.ref, *ptrs, psl, S, pst, py)
+    _step(dev, _lib().kda_sscan_step, state, plan.ref, *ptrs, psl, S, pst, py)
     return y
 
 
@@ -460,5 +470,5 @@ def kda_step(q, k, v, g, beta, state, slots=None, scale=None, beta_logits=False)
     scale = None if scale is None else float(scale)
     _, d = _kda_dims(B, H, HV, K, V, scale, "f32" if dt is F32 else "bf16", bool(beta_logits))
     o, po = _like(v)
-    _launch(dev, _lib().kda_step, d, *ptrs, S, pst, po)
+    _step(dev, _lib().kda_step, state, d, *ptrs, S, pst, po)
     return o
