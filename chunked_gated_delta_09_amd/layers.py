@@ -37,6 +37,14 @@ _DT = {torch.float32: 0, torch.bfloat16: 1}
 
 _i32, _i64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 _pi32 = ctypes.POINTER(_i32)
+_I32_MAX = 2 ** 31 - 1
+
+
+def _fit(name, v):
+    """Refuses a size that ctypes would cut to its low 32 bits, and so to another call."""
+    if not -_I32_MAX <= v <= _I32_MAX:
+        raise ValueError(f"{name} ({v}) does not fit 32 bits")
+    return v
 
 
 class _ConvDims(ctypes.Structure):
@@ -177,6 +185,8 @@ def _cuts(cu_seqlens, cu_seqlens_dev, B, dev):
     cu = [int(c) for c in (cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens)]
     if len(cu) < 2:
         raise ValueError("cu_seqlens needs at least two entries")
+    _fit("cu_seqlens", min(cu))
+    _fit("cu_seqlens", max(cu))
     if cu_seqlens_dev is None:
         cu_seqlens_dev = torch.tensor(cu, dtype=torch.int32, device=f"cuda:{dev}")
     ptr = _need(cu_seqlens_dev, "cu_seqlens_dev", torch.int32, (len(cu),), dev)
@@ -189,6 +199,9 @@ class _Plan:
     __slots__ = ("dims", "ref", "sizes")
 
     def __init__(self, kind, *values):
+        for (name, field), v in zip(kind._fields_, values):
+            if field is _i32:
+                _fit(name, v)
         self.dims = kind(*values)
         self.ref = ctypes.byref(self.dims)
         self.sizes = {}
@@ -214,6 +227,8 @@ def _plan_of(kind, cu_dev, cu_host, before, after):
 
 @functools.lru_cache(maxsize=512)
 def _kda_dims(B, H, HV, K, V, scale, dtype, beta_logits):
+    for name, v in (("B", B), ("H", H), ("HV", HV), ("K", K), ("V", V)):
+        _fit(name, v)
     d, _ = make_dims(B, 1, H, HV, K, V, 16, scale, dtype, beta_logits=beta_logits)
     return d, ctypes.byref(d)
 
@@ -314,7 +329,7 @@ def short_conv_step(x, state, weight, bias=None, slots=None, activation="silu"):
     psl = _need(slots, "slots", torch.int32, (B,), dev)
     plan = _plan(_ConvDims, B, 1, D, W, B, None, None, row, _act(activation, (None, "silu")), _DT[x.dtype])
     y, py = _like(x, row)
-    _step(dev, _lib().kda_short_conv_step, state, plan.ref, px, pw, pb, psl, S, pst, py)
+    _step(dev, _lib().kda_short_conv_step, state, plan.ref, px, pw, pb, psl, _fit("S", S), pst, py)
     return y
 
 
@@ -404,7 +419,7 @@ def selective_scan_step(x, dt, A, B, C, state, slots=None, skip=None, z=None, dt
     pst = _need(state, "state", F32, (S, D, NS), dev)
     psl = _need(slots, "slots", torch.int32, rows, dev)
     y, py = _like(x, strides[0])
-    _step(dev, _lib().kda_sscan_step, state, plan.ref, *ptrs, psl, S, pst, py)
+    _step(dev, _lib().kda_sscan_step, state, plan.ref, *ptrs, psl, _fit("S", S), pst, py)
     return y
 
 
@@ -470,5 +485,5 @@ def kda_step(q, k, v, g, beta, state, slots=None, scale=None, beta_logits=False)
     scale = None if scale is None else float(scale)
     _, d = _kda_dims(B, H, HV, K, V, scale, "f32" if dt is F32 else "bf16", bool(beta_logits))
     o, po = _like(v)
-    _step(dev, _lib().kda_step, state, d, *ptrs, S, pst, po)
+    _step(dev, _lib().kda_step, state, d, *ptrs, _fit("S", S), pst, po)
     return o

@@ -67,3 +67,54 @@ def test_steps_tell_autograd_that_the_state_changed(launched, name):
         loss.backward()
     with torch.inference_mode():
         step_call(name, on_gpu(*STATES[name]))  # a tensor without a version
+
+
+class Sized:
+    """Stands in for a GPU tensor too large for this machine: its description, and no memory."""
+
+    is_cuda, device, requires_grad = True, "cuda:0", False
+
+    def __init__(self, *shape, dtype=torch.bfloat16):
+        self.shape, self.dtype = torch.Size(shape), dtype
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 256
+
+    def new_empty(self, shape, dtype=None):
+        return Sized(*shape, dtype=dtype or self.dtype)
+
+
+WRAPPED = 2 ** 32 + 16  # an int32 field that takes it without a look holds 16
+
+
+@pytest.mark.parametrize("what,call", [
+    ("T", lambda: layers.short_conv(Sized(1, WRAPPED, 8), on_gpu(8, 4))),
+    ("T", lambda: layers.short_conv_bwd(Sized(1, WRAPPED, 8), on_gpu(8, 4), Sized(1, WRAPPED, 8))),
+    ("B", lambda: layers.short_conv(Sized(WRAPPED, 1, 8), on_gpu(8, 4))),
+    ("T", lambda: layers.selective_scan(*[Sized(1, WRAPPED, 8)] * 2, on_gpu(8, 4), *[Sized(1, WRAPPED, 1, 4)] * 2)),
+    ("C", lambda: layers.group_norm(Sized(1, WRAPPED), 1)),
+    ("G", lambda: layers.group_norm(Sized(1, WRAPPED), WRAPPED)),
+    ("S", lambda: step_call("short_conv_step", Sized(WRAPPED, 3, 8, dtype=torch.float32))),
+    ("S", lambda: step_call("selective_scan_step", Sized(WRAPPED, 8, 4, dtype=torch.float32))),
+    ("S", lambda: step_call("kda_step", Sized(WRAPPED, 4, 16, 8, dtype=torch.float32))),
+    ("B", lambda: layers.kda_step(*[Sized(WRAPPED, 1, 1)] * 3, Sized(WRAPPED, 1, 1, dtype=torch.float32),
+                                  Sized(WRAPPED, 1, dtype=torch.float32), on_gpu(1, 1, 1, 1))),
+    ("cu_seqlens", lambda: layers.short_conv(on_gpu(1, 16, 8), on_gpu(8, 4), cu_seqlens=[0, WRAPPED],
+                                             cu_seqlens_dev=torch.zeros(2, dtype=torch.int32).as_subclass(OnGpu)))])
+def test_sizes_that_do_not_fit_32_bits_are_refused(launched, monkeypatch, what, call):
+    monkeypatch.setattr(torch, "empty_like", lambda t: t.new_empty(t.shape))
+    with pytest.raises(ValueError, match=rf"{what}\b.*32 bits"):
+        call()
+    assert not launched
