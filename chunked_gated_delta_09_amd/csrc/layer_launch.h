@@ -115,6 +115,7 @@ struct NormArgs {
 struct NormPlan {
   int tpi, nch, vec;       // lanes of a group, chunks a lane holds, elements of a chunk
   int64_t blocks;          // workgroups
+  int64_t stride;          // groups of lanes that take items: a multiple of G
   int64_t part_rows;       // rows of partial sums
   int part_cols;           // columns of one of the two sums
 };

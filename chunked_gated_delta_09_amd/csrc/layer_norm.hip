@@ -153,14 +153,14 @@ __device__ __forceinline__ float normalise(const NormArgs& a, const Place<VEC, N
 }
 
 // A group of lanes takes the items sub, sub + stride, ... with stride a multiple of G, so its channels
-// (and the weights in its registers) stay the same; the next item is loaded while this one is worked on.
+// (and the weights in its registers) stay the same; the next item is loaded while this one is worked on. The
+// last workgroup may have groups of lanes behind the stride: they take none.
 template <class T, int VEC, int NCH, int THREADS, bool NEAR>
 __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormArgs a, int tpi, int64_t stride) {
   __shared__ float sh[32];
   const int lane = threadIdx.x % tpi;
   const int64_t sub = (int64_t)blockIdx.x * (THREADS / tpi) + threadIdx.x / tpi;
-  const int64_t items = a.R * a.G;
-  if (sub >= items) return;  // whole groups of lanes leave; a workgroup-wide group always has its item
+  if (sub >= stride) return;  // whole groups of lanes leave; a workgroup-wide group always has its item
   const int g = (int)(sub % a.G);
   const Place<VEC, NEAR> pl{lane, tpi, a.C, a.vec != 0};
   const int64_t pat = a.shared ? 0 : (int64_t)g * a.C, step = stride / a.G;
@@ -211,18 +211,19 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormArgs a, int tpi, 
   const int64_t sub = (int64_t)blockIdx.x * subs + threadIdx.x / tpi;
   const int g = (int)(sub % a.G);
   const Place<VEC, NEAR> pl{lane, tpi, a.C, a.vec != 0};
-  const int64_t items = a.R * a.G, step = stride / a.G;
+  const int64_t step = stride / a.G;
   const float inv = 1.f / (float)a.C;
   float w[NCH][VEC], b[NCH][VEC], dw[NCH][VEC], db[NCH][VEC];
   const int64_t pat = a.shared ? 0 : (int64_t)g * a.C;
-  int64_t row = sub / a.G;
+  const bool used = sub < stride;
+  int64_t row = used ? sub / a.G : a.R;
   Raw<T, VEC, NCH> rx, rg, rd;
   auto fetch = [&](int64_t r) {
     rx.load(a.x, r * a.x_row + (int64_t)g * a.C, pl);
     rd.load(a.dy, (r * a.G + g) * a.C, pl);
     if (a.gate != nullptr) rg.load(a.gate, r * a.gate_row + (int64_t)g * a.C, pl);
   };
-  if (sub < items) fetch(row);
+  if (used) fetch(row);
   load_param<VEC, NCH, NEAR>(a.w, 1.f, pat, pl, a.wvec != 0, w);
   load_param<VEC, NCH, NEAR>(a.bias, 0.f, pat, pl, a.wvec != 0, b);
   const Act act(a.act);
@@ -283,6 +284,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormArgs a, int tpi, 
   }
   if (a.part == nullptr) return;
   if (!a.shared || subs == 1) {
+    if (!used) return;
     float* p = a.part + sub * 2 * a.C;
     if (!a.shared) p = a.part + ((sub / a.G) * 2 * a.G + g) * (int64_t)a.C;
     const int64_t second = a.shared ? a.C : (int64_t)a.G * a.C;
@@ -348,11 +350,10 @@ __global__ __launch_bounds__(1024) void col_sum_kernel(const float* in, int64_t 
 template <class T, int VEC, int NCH, int THREADS>
 hipError_t norm_fwd_t(const NormArgs& a, const NormPlan& p, hipStream_t st) {
   const dim3 grid((unsigned)p.blocks), block(THREADS);
-  const int64_t stride = p.blocks * (THREADS / p.tpi);
   if (a.C % VEC == 0)
-    hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, NCH, THREADS, true>), grid, block, 0, st, a, p.tpi, stride);
+    hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, NCH, THREADS, true>), grid, block, 0, st, a, p.tpi, p.stride);
   else
-    hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, NCH, THREADS, false>), grid, block, 0, st, a, p.tpi, stride);
+    hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, NCH, THREADS, false>), grid, block, 0, st, a, p.tpi, p.stride);
   return hipGetLastError();
 }
 
@@ -361,11 +362,10 @@ hipError_t norm_bwd_t(const NormArgs& a, const NormPlan& p, hipStream_t st) {
   const int subs = THREADS / p.tpi;
   const size_t lds = sizeof(float) * (64 + (a.shared && subs > 1 ? (size_t)subs * a.C : 0));
   const dim3 grid((unsigned)p.blocks), block(THREADS);
-  const int64_t stride = p.blocks * subs;
   if (a.C % VEC == 0)
-    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, NCH, THREADS, true>), grid, block, lds, st, a, p.tpi, stride);
+    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, NCH, THREADS, true>), grid, block, lds, st, a, p.tpi, p.stride);
   else
-    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, NCH, THREADS, false>), grid, block, lds, st, a, p.tpi, stride);
+    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, NCH, THREADS, false>), grid, block, lds, st, a, p.tpi, p.stride);
   return hipGetLastError();
 }
 
@@ -384,9 +384,9 @@ hipError_t norm_bwd_t(const NormArgs& a, const NormPlan& p, hipStream_t st) {
 }  // namespace
 
 // Lanes of a group: enough for one chunk of 16 bytes each up to a wave, for two chunks up to two waves'
-// worth, then a workgroup of 256 and of 1024 in the same way. Workgroups: up to eight a CU of 256, a
-// whole number of rows' groups together (the lanes of a group stay on its channels), none without an
-// item.
+// worth, then a workgroup of 256 and of 1024 in the same way. Workgroups: up to eight a CU of 256, taking
+// whole rows side by side (the lanes of a group stay on its channels); a row of more groups than that has
+// workgroups for all of them.
 bool norm_plan(int dtype, int64_t R, int G, int C, int shared, bool bwd, NormPlan* p) {
   p->vec = dtype == KDA_F32 ? 4 : 8;
   const int chunks = (C + p->vec - 1) / p->vec;
@@ -397,14 +397,6 @@ bool norm_plan(int dtype, int64_t R, int G, int C, int shared, bool bwd, NormPla
   p->nch = chunks > p->tpi ? 2 : 1;
   if (chunks > 2 * p->tpi) return false;
   const int64_t subs = p->tpi == 1024 ? 1 : 256 / p->tpi;
-  // workgroups in steps of G / gcd(G, subs)
-  int64_t g = G, h = subs;
-  while (h) {
-    const int64_t r = g % h;
-    g = h;
-    h = r;
-  }
-  const int64_t step = G / g;
   const int64_t most = (R * G + subs - 1) / subs;
   int64_t full = p->tpi == 1024 ? 512 : 2048;
   if (bwd) {
@@ -412,11 +404,13 @@ bool norm_plan(int dtype, int64_t R, int G, int C, int shared, bool bwd, NormPla
     full /= 2;
     if (most / 4 < full) full = most / 4 > 256 ? most / 4 : 256;
   }
-  int64_t blocks = (full + step - 1) / step * step;
-  if (blocks > most) blocks = (most + step - 1) / step * step;
-  p->blocks = blocks;
+  // rows whose groups are taken side by side: as many as fill those workgroups, rounded up, and there are
+  int64_t rows = (full * subs + G - 1) / G;
+  if (rows > R) rows = R;
+  p->stride = rows * G;
+  p->blocks = (p->stride + subs - 1) / subs;
   p->part_cols = shared ? C : G * C;
-  p->part_rows = shared ? blocks : blocks * subs / G;
+  p->part_rows = shared ? p->blocks : rows;
   return true;
 }
 
