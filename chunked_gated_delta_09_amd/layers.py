@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 
 import torch
 
@@ -62,6 +63,9 @@ class _NormDims(ctypes.Structure):
     _fields_ = [("R", _i64), ("G", _i32), ("C", _i32), ("center", _i32), ("act", _i32), ("shared", _i32), ("eps", _f32),
                 ("x_row", _i64), ("gate_row", _i64), ("dtype", _i32)]
 
+
+for _kind in (_ConvDims, _ScanDims, _NormDims):  # what 32-bit fields are given, of all values of a structure
+    _kind.narrow = operator.itemgetter(*[i for i, (_, field) in enumerate(_kind._fields_) if field is _i32])
 
 _ready = None
 
@@ -185,8 +189,8 @@ def _cuts(cu_seqlens, cu_seqlens_dev, B, dev):
     cu = [int(c) for c in (cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens)]
     if len(cu) < 2:
         raise ValueError("cu_seqlens needs at least two entries")
-    _fit("cu_seqlens", min(cu))
-    _fit("cu_seqlens", max(cu))
+    if max(cu) > _I32_MAX or min(cu) < -_I32_MAX:
+        raise ValueError("cu_seqlens holds a cut that does not fit 32 bits")
     if cu_seqlens_dev is None:
         cu_seqlens_dev = torch.tensor(cu, dtype=torch.int32, device=f"cuda:{dev}")
     ptr = _need(cu_seqlens_dev, "cu_seqlens_dev", torch.int32, (len(cu),), dev)
@@ -199,9 +203,10 @@ class _Plan:
     __slots__ = ("dims", "ref", "sizes")
 
     def __init__(self, kind, *values):
-        for (name, field), v in zip(kind._fields_, values):
-            if field is _i32:
-                _fit(name, v)
+        if max(kind.narrow(values)) > _I32_MAX:
+            for (name, field), v in zip(kind._fields_, values):
+                if field is _i32:
+                    _fit(name, v)
         self.dims = kind(*values)
         self.ref = ctypes.byref(self.dims)
         self.sizes = {}
