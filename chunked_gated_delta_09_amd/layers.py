@@ -23,7 +23,6 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import operator
 
 import torch
 
@@ -63,9 +62,6 @@ class _NormDims(ctypes.Structure):
     _fields_ = [("R", _i64), ("G", _i32), ("C", _i32), ("center", _i32), ("act", _i32), ("shared", _i32), ("eps", _f32),
                 ("x_row", _i64), ("gate_row", _i64), ("dtype", _i32)]
 
-
-for _kind in (_ConvDims, _ScanDims, _NormDims):  # what 32-bit fields are given, of all values of a structure
-    _kind.narrow = operator.itemgetter(*[i for i, (_, field) in enumerate(_kind._fields_) if field is _i32])
 
 _ready = None
 
@@ -186,7 +182,7 @@ def _cuts(cu_seqlens, cu_seqlens_dev, B, dev):
         return B, None, None, None
     if B != 1:
         raise ValueError("packed sequences need batch size 1")
-    cu = [int(c) for c in (cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens)]
+    cu = list(map(int, cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens))
     if len(cu) < 2:
         raise ValueError("cu_seqlens needs at least two entries")
     if max(cu) > _I32_MAX or min(cu) < -_I32_MAX:
@@ -203,10 +199,6 @@ class _Plan:
     __slots__ = ("dims", "ref", "sizes")
 
     def __init__(self, kind, *values):
-        if max(kind.narrow(values)) > _I32_MAX:
-            for (name, field), v in zip(kind._fields_, values):
-                if field is _i32:
-                    _fit(name, v)
         self.dims = kind(*values)
         self.ref = ctypes.byref(self.dims)
         self.sizes = {}
@@ -221,12 +213,19 @@ class _Plan:
 
 
 # Those of calls without cuts are kept, by their values alone: the library only reads them.
-_plan = functools.lru_cache(maxsize=512)(_Plan)
+@functools.lru_cache(maxsize=512)
+def _plan(kind, *values):
+    for (name, field), v in zip(kind._fields_, values):
+        if field is _i32:
+            _fit(name, v)
+    return _Plan(kind, *values)
 
 
 def _plan_of(kind, cu_dev, cu_host, before, after):
     if cu_host is None:
         return _plan(kind, *before, None, None, *after)
+    if max(before) > _I32_MAX:
+        raise ValueError(f"{max(before)} does not fit 32 bits, among {[n for n, _ in kind._fields_[:len(before)]]}")
     return _Plan(kind, *before, cu_dev, cu_host, *after)
 
 

@@ -111,6 +111,8 @@ WRAPPED = 2 ** 32 + 16  # an int32 field that takes it without a look holds 16
     ("S", lambda: step_call("kda_step", Sized(WRAPPED, 4, 16, 8, dtype=torch.float32))),
     ("B", lambda: layers.kda_step(*[Sized(WRAPPED, 1, 1)] * 3, Sized(WRAPPED, 1, 1, dtype=torch.float32),
                                   Sized(WRAPPED, 1, dtype=torch.float32), on_gpu(1, 1, 1, 1))),
+    (str(WRAPPED), lambda: layers.short_conv(Sized(1, WRAPPED, 8), on_gpu(8, 4), cu_seqlens=[0, 16],
+                                             cu_seqlens_dev=torch.zeros(2, dtype=torch.int32).as_subclass(OnGpu))),
     ("cu_seqlens", lambda: layers.short_conv(on_gpu(1, 16, 8), on_gpu(8, 4), cu_seqlens=[0, WRAPPED],
                                              cu_seqlens_dev=torch.zeros(2, dtype=torch.int32).as_subclass(OnGpu)))])
 def test_sizes_that_do_not_fit_32_bits_are_refused(launched, monkeypatch, what, call):
