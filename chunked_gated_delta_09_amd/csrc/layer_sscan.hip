@@ -128,6 +128,14 @@ __device__ __forceinline__ void store_states(float* p, int64_t row, int N, int p
     if (part * NPL + i < N) p[row * N + part * NPL + i] = v[i];
 }
 
+// h 2^e, for e of any size: over a segment 2^e alone can be past fp32 where the product is not, and is zero where h
+// is. The fraction's factor is in (1/2, 1], the rest goes into the exponent. (A NaN in e is one in what the
+// segment adds, too.)
+__device__ __forceinline__ float times_exp2(float h, float e) {
+  const float low = fmaxf(e, -1024.f), whole = ceilf(low);
+  return ldexpf(h * exp2_hw(low - whole), (int)whole);
+}
+
 // Carries h through `count` segments from `s` on (step: the one behind or before): h <- exp(A sum dt) h +
 // loc. Eight segments are loaded together, since only the sums depend on each other.
 template <int NP>
@@ -148,7 +156,7 @@ __device__ __forceinline__ void join_segments(const ScanArgs& a, int64_t s, int 
       if (k + u < count) {
         const float add[NPL] = {loc[u].x, loc[u].y, loc[u].z, loc[u].w};
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) h[i] = fmaf(exp2_hw(sum[u] * A2[i]), h[i], add[i]);
+        for (int i = 0; i < NPL; ++i) h[i] = times_exp2(h[i], sum[u] * A2[i]) + add[i];
       }
   }
 }

@@ -29,3 +29,34 @@ def test_group_norm_groups_that_do_not_divide(dtype, R, G, C, opts):
     r = layers.group_norm_bwd(x, G, dy, **kw)
     for k, v in gr.items():
         ref.close(r[k], v, dtype if k == "dx" else F32, 64 if k == "dx" else ops(R * G), k)
+
+
+OUT = dict(x="dx", dt="ddt", A="dA", B="dB", C="dC", skip="dskip", z="dz", dt_bias="ddt_bias", h0="dh0")
+
+
+@pytest.mark.parametrize("cu", [None, [0, 300, 300, 301, 700]], ids=["dense", "packed"])
+def test_selective_scan_growth_of_nothing(cu):
+    """A factor of e^6 a token on states that stay zero, because nothing comes in before a sequence's last two tokens,
+    and on gradients that stay zero behind its first two. Over a segment of 16 tokens the factor is past fp32; what
+    it carries is zero all the same."""
+    T, D, NS = 700, 8, 8
+    d = Draw(73)
+    first, last = torch.zeros(1, T, 1), torch.zeros(1, T, 1)
+    cuts = ref.cuts_of(1, T, cu)
+    for lo, hi in zip(cuts[:-1], cuts[1:]):
+        first[0, lo:min(lo + 2, hi)] = 1.0
+        last[0, max(hi - 2, lo):hi] = 1.0
+    g = d.g
+    host = dict(x=torch.randn(1, T, D, generator=g) * last, dt=torch.full((1, T, D), -6.0), A=torch.full((D, NS), -1.0),
+                B=torch.randn(1, T, 1, NS, generator=g), C=torch.randn(1, T, 1, NS, generator=g))
+    dy = torch.randn(1, T, D, generator=g) * first
+    dev = {k: v.cuda() for k, v in host.items()}
+    leaf = {k: v.to(ref.F64).requires_grad_() for k, v in host.items()}
+    y64, f64 = ref.scan(*leaf.values(), None, None, None, None, False, cu)
+    gr = dict(zip(leaf, grads((y64,), (dy.to(ref.F64),), list(leaf.values()))))
+    f = layers.selective_scan(**dev, cu_seqlens=cu, save=True)
+    r = layers.selective_scan_bwd(**dev, states=f["states"], dy=dy.cuda(), cu_seqlens=cu)
+    ref.close(f["y"], y64, F32, ops(2), "y")
+    ref.close(f["final_state"], f64, F32, ops(2), "final_state")
+    for k, v in gr.items():
+        ref.close(r[OUT[k]], v, F32, ops(2), k)
