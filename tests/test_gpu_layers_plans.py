@@ -5,7 +5,8 @@ import torch
 
 from chunked_gated_delta_09_amd import layers
 from tests import layer_ref as ref
-from tests.test_gpu_layers import BF16, F32, Draw, grads, ops
+from tests.test_gpu_layers import BF16, F32, SEQS, Draw, grads, ops
+from tests.test_layers_plan import CUT, scan_plan
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +61,56 @@ def test_selective_scan_growth_of_nothing(cu):
     ref.close(f["final_state"], f64, F32, ops(2), "final_state")
     for k, v in gr.items():
         ref.close(r[OUT[k]], v, F32, ops(2), k)
+
+
+def check_scan(v, dy, df, dtype, cu, softplus):
+    """The scan and its backward against 64 bits; v: each input on the GPU and as a 64-bit leaf."""
+    dev = {k: t[0] for k, t in v.items()}
+    names = [k for k in v if v[k][1] is not None]
+    y64, f64 = ref.scan(*(v[k][1] for k in ("x", "dt", "A", "B", "C", "skip", "z", "dt_bias", "h0")), softplus, cu)
+    gr = dict(zip(names, grads((y64, f64), (dy[1], df[1]), [v[k][1] for k in names])))
+    f = layers.selective_scan(**dev, cu_seqlens=cu, dt_softplus=softplus, save=True)
+    dev.pop("h0")
+    r = layers.selective_scan_bwd(**dev, states=f["states"], dy=dy[0], dfinal=df[0], cu_seqlens=cu, dt_softplus=softplus,
+                                  output_dh0=True)
+    B, T = dy[0].shape[:2]
+    cuts = ref.cuts_of(B, T, cu)
+    longest = max(hi - lo for lo, hi in zip(cuts[:-1], cuts[1:]))
+    ref.close(f["y"], y64, dtype, ops(longest), "y")
+    ref.close(f["final_state"], f64, F32, ops(longest), "final_state")
+    for k in names:
+        whole = k in ("A", "skip", "dt_bias")
+        ref.close(r[OUT[k]], gr[k], F32 if whole or k == "h0" else dtype, ops(B * T if whole else longest), k)
+
+
+@pytest.mark.parametrize("name,dtype", [(n, F32) for n in CUT] + [("quarters", BF16), ("packed_quarters", BF16)])
+def test_selective_scan_segments(name, dtype):
+    """Segments of several chunks, and local ones of a half and a quarter of them, with a remainder at the end and
+    states that live through all of it: about half of a state is left after a segment."""
+    lens, packed, D, NS, G, fwd, bwd = CUT[name]
+    assert (scan_plan(lens, D, NS, G, False)[:2], scan_plan(lens, D, NS, G, True)[:2]) == (fwd, bwd)
+    cu = [sum(lens[:i]) for i in range(len(lens) + 1)] if packed else None
+    B, T, N = (1, cu[-1], len(lens)) if packed else (len(lens), lens[0], len(lens))
+    d = Draw(79)
+    A = -torch.rand(D, NS, generator=d.g) * 3 / bwd[0]
+    v = dict(x=d(B, T, D, dtype=dtype), dt=d(B, T, D, dtype=dtype, std=0.5), A=(A.cuda(), A.to(ref.F64).requires_grad_()),
+             B=d(B, T, G, NS, dtype=dtype), C=d(B, T, G, NS, dtype=dtype), skip=d(D), z=d(B, T, D, dtype=dtype),
+             dt_bias=d(D, std=0.5, mean=-1.0), h0=d(N, D, NS))
+    check_scan(v, d(B, T, D, dtype=dtype, leaf=False), d(N, D, NS, leaf=False), dtype, cu, True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("seqs", list(SEQS))
+def test_selective_scan_one_state_and_a_bias(dtype, seqs):
+    """One state a channel, four groups, a bias of the steps without softplus; all steps above zero."""
+    B, T, cu = SEQS[seqs]
+    D, NS, G, N = 132, 1, 4, len(cu) - 1 if cu else B
+    d = Draw(83)
+    A = -torch.rand(D, NS, generator=d.g) - 0.1
+    dt = (torch.rand(B, T, D, generator=d.g) * 0.3 + 0.2).to(dtype)
+    bias = torch.rand(D, generator=d.g) * 0.2 - 0.1
+    none = (None, None)
+    v = dict(x=d(B, T, D, dtype=dtype), dt=(dt.cuda(), dt.to(ref.F64).requires_grad_()),
+             A=(A.cuda(), A.to(ref.F64).requires_grad_()), B=d(B, T, G, NS, dtype=dtype), C=d(B, T, G, NS, dtype=dtype),
+             skip=none, z=none, dt_bias=(bias.cuda(), bias.to(ref.F64).requires_grad_()), h0=d(N, D, NS))
+    check_scan(v, d(B, T, D, dtype=dtype, leaf=False), d(N, D, NS, leaf=False), dtype, cu, False)
