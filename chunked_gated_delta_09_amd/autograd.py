@@ -125,7 +125,13 @@ class SelectiveScanFunction(torch.autograd.Function):
 
 def selective_scan(x, dt, A, B, C, skip=None, z=None, dt_bias=None, h0=None, cu_seqlens=None, cu_seqlens_dev=None,
                    dt_softplus=False, output_final_state=True):
-    """Differentiable ``layers.selective_scan``. Returns (y, final_state or None)."""
+    """Differentiable ``layers.selective_scan``. Returns (y, final_state or None). The states of the chunks are
+    kept (and written) where a backward can follow."""
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, dt, A, B, C, skip, z, dt_bias, h0))):
+        f = layers.selective_scan(x, dt, A, B, C, skip=skip, z=z, dt_bias=dt_bias, h0=h0, cu_seqlens=cu_seqlens,
+                                  cu_seqlens_dev=cu_seqlens_dev, dt_softplus=dt_softplus,
+                                  output_final_state=output_final_state, save=False)
+        return f["y"], f["final_state"]
     return SelectiveScanFunction.apply(x, dt, A, B, C, skip, z, dt_bias, h0, cu_seqlens, cu_seqlens_dev, dt_softplus,
                                        output_final_state)
 

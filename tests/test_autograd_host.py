@@ -85,3 +85,23 @@ def test_kda_chunk_keeps_its_cuts_and_scale(monkeypatch, kind):
     o.sum().backward()
     assert [c["cu_seqlens"] for c in calls] == [CUTS, CUTS]
     assert [float(c["scale"]) for c in calls] == [0.5, 0.5]
+
+
+NONE = dict(dskip=lambda: None, dz=lambda: None, ddt_bias=lambda: None, dh0=lambda: None)
+SCAN = (dict(y=zeros(1, 5, 3), final_state=lambda: None, states=zeros(3, 3, 2)),
+        dict(dx=zeros(1, 5, 3), ddt=zeros(1, 5, 3), dA=zeros(3, 2), dB=zeros(1, 5, 1, 2), dC=zeros(1, 5, 1, 2), **NONE))
+
+
+def test_selective_scan_saves_states_for_a_backward_only(monkeypatch):
+    """Without gradients there is no backward to keep the chunks' states for."""
+    calls = record(monkeypatch, ag.layers, ("selective_scan", "selective_scan_bwd"), SCAN)
+    x, A, B = torch.zeros(1, 5, 3), torch.zeros(3, 2), torch.zeros(1, 5, 1, 2)
+    leaf = A.clone().requires_grad_()
+    ag.selective_scan(x, x, A, B, B)
+    with torch.no_grad():
+        ag.selective_scan(x, x, leaf, B, B)
+    with torch.inference_mode():
+        ag.selective_scan(x, x, leaf, B, B)
+    ag.selective_scan(x, x, leaf, B, B)[0].sum().backward()
+    ag.selective_scan(x, x, A, B, B, h0=torch.zeros(1, 3, 2, requires_grad=True))
+    assert [c["save"] for c in calls if "save" in c] == [False, False, False, True, True]
