@@ -68,12 +68,20 @@ def kda_chunk(q, k, v, g, beta, h0=None, cu_seqlens=None, C=64, scale=None, outp
                                   save_operands)
 
 
+def _kept_both(cu_seqlens, cu_seqlens_dev, device):
+    """The cuts as _kept has them, and one copy of them on the GPU for the forward and the backward."""
+    cu_seqlens = _kept(cu_seqlens)
+    if cu_seqlens is not None and cu_seqlens_dev is None:
+        cu_seqlens_dev = torch.tensor(cu_seqlens, dtype=torch.int32, device=device)
+    return cu_seqlens, cu_seqlens_dev
+
+
 class ShortConvFunction(torch.autograd.Function):
     """y, final_state = short_conv(x, weight, bias, h0) with gradients for all four."""
 
     @staticmethod
     def forward(ctx, x, weight, bias, h0, cu_seqlens, cu_seqlens_dev, activation, output_final_state):
-        cu_seqlens = _kept(cu_seqlens)
+        cu_seqlens, cu_seqlens_dev = _kept_both(cu_seqlens, cu_seqlens_dev, x.device)
         f = layers.short_conv(x, weight, bias=bias, h0=h0, cu_seqlens=cu_seqlens, cu_seqlens_dev=cu_seqlens_dev,
                               activation=activation, output_final_state=output_final_state)
         ctx.save_for_backward(x, weight, bias, h0, cu_seqlens_dev)
@@ -102,7 +110,7 @@ class SelectiveScanFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, dt, A, B, C, skip, z, dt_bias, h0, cu_seqlens, cu_seqlens_dev, dt_softplus, output_final_state):
-        cu_seqlens = _kept(cu_seqlens)
+        cu_seqlens, cu_seqlens_dev = _kept_both(cu_seqlens, cu_seqlens_dev, x.device)
         f = layers.selective_scan(x, dt, A, B, C, skip=skip, z=z, dt_bias=dt_bias, h0=h0, cu_seqlens=cu_seqlens,
                                   cu_seqlens_dev=cu_seqlens_dev, dt_softplus=dt_softplus,
                                   output_final_state=output_final_state, save=True)

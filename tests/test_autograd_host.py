@@ -105,3 +105,19 @@ def test_selective_scan_saves_states_for_a_backward_only(monkeypatch):
     ag.selective_scan(x, x, leaf, B, B)[0].sum().backward()
     ag.selective_scan(x, x, A, B, B, h0=torch.zeros(1, 3, 2, requires_grad=True))
     assert [c["save"] for c in calls if "save" in c] == [False, False, False, True, True]
+
+
+@pytest.mark.parametrize("given", [False, True], ids=["made", "given"])
+@pytest.mark.parametrize("op", ["short_conv", "selective_scan"])
+def test_one_device_copy_of_the_cuts(monkeypatch, op, given):
+    """The backward takes the copy that the forward took, the caller's or the one made for it."""
+    conv = (dict(y=zeros(1, 5, 3), final_state=lambda: None),
+            dict(dx=zeros(1, 5, 3), dweight=zeros(3, 4), dbias=lambda: None, dh0=lambda: None))
+    calls = record(monkeypatch, ag.layers, (op, op + "_bwd"), conv if op == "short_conv" else SCAN)
+    x, A, B = torch.zeros(1, 5, 3, requires_grad=True), torch.zeros(3, 2), torch.zeros(1, 5, 1, 2)
+    cu_dev = torch.tensor(CUTS, dtype=torch.int32) if given else None
+    args = (x, torch.zeros(3, 4)) if op == "short_conv" else (x, x.detach(), A, B, B)
+    getattr(ag, op)(*args, cu_seqlens=CUTS, cu_seqlens_dev=cu_dev)[0].sum().backward()
+    fwd, bwd = (c["cu_seqlens_dev"] for c in calls)
+    assert fwd.dtype == torch.int32 and fwd.tolist() == CUTS
+    assert fwd.data_ptr() == bwd.data_ptr() == (cu_dev if given else fwd).data_ptr()
