@@ -105,6 +105,15 @@ def short_conv(x, weight, bias=None, h0=None, cu_seqlens=None, cu_seqlens_dev=No
     return ShortConvFunction.apply(x, weight, bias, h0, cu_seqlens, cu_seqlens_dev, activation, output_final_state)
 
 
+def _rows16(t):
+    """A gradient of states as the library reads it: contiguous, and 16-byte aligned, which a view of a larger gradient
+    may not be."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 class SelectiveScanFunction(torch.autograd.Function):
     """y, final_state = selective_scan(x, dt, A, B, C, skip, z, dt_bias, h0) with gradients for all nine."""
 
@@ -125,7 +134,7 @@ class SelectiveScanFunction(torch.autograd.Function):
         x, dt, A, B, C, skip, z, dt_bias, cu_dev, states = ctx.saved_tensors
         dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
         r = layers.selective_scan_bwd(x, dt, A, B, C, states, dy, skip=skip, z=z, dt_bias=dt_bias,
-                                      dfinal=None if dfinal is None else dfinal.contiguous(), cu_seqlens=ctx.cu_seqlens,
+                                      dfinal=_rows16(dfinal), cu_seqlens=ctx.cu_seqlens,
                                       cu_seqlens_dev=cu_dev, dt_softplus=ctx.dt_softplus, output_dh0=ctx.has_h0)
         return (r["dx"], r["ddt"], r["dA"], r["dB"], r["dC"], r["dskip"], r["dz"], r["ddt_bias"], r["dh0"], None, None,
                 None, None)

@@ -5,7 +5,8 @@ model runs (``*_step``, with KDA's own as ``kda_step``).
 Argument marshalling over the C ABI in ``include/kda_layers.h``; every step of the computation is a
 HIP kernel of the library. Tensors are on one GPU, whose current stream the call is enqueued on.
 They are contiguous, except that ``x``, ``dt``, ``z``, ``B``, ``C`` and ``gate`` may be column slices
-of a wider contiguous tensor (``proj[..., a:b]``).
+of a wider contiguous tensor (``proj[..., a:b]``). A scan's fp32 tensors [..., NS] with NS of 8, 16, 32 or 64 begin
+on a multiple of 16 bytes, as tensors of their own do.
 
 Packed sequences: ``cu_seqlens`` is the host list of cuts, with batch size 1; a caller that has a
 device copy (int32) passes it as ``cu_seqlens_dev``, otherwise the call makes one (which copies

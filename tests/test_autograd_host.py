@@ -121,3 +121,19 @@ def test_one_device_copy_of_the_cuts(monkeypatch, op, given):
     fwd, bwd = (c["cu_seqlens_dev"] for c in calls)
     assert fwd.dtype == torch.int32 and fwd.tolist() == CUTS
     assert fwd.data_ptr() == bwd.data_ptr() == (cu_dev if given else fwd).data_ptr()
+
+
+def test_selective_scan_backward_aligns_the_final_states_gradient(monkeypatch):
+    """torch hands a backward views: behind a concatenation the gradient of the final state begins where the parts before
+    it end, while the library reads its rows 16 bytes at a time."""
+    seen = []
+    x, A, B = torch.zeros(1, 5, 3, requires_grad=True), torch.zeros(3, 8), torch.zeros(1, 5, 1, 8)
+    monkeypatch.setattr(ag.layers, "selective_scan", lambda *a, **kw: dict(
+        y=torch.zeros(1, 5, 3), final_state=torch.zeros(1, 3, 8), states=torch.zeros(1, 3, 8)))
+    monkeypatch.setattr(ag.layers, "selective_scan_bwd", lambda *a, dfinal, **kw: seen.append(dfinal) or {
+        k: v() for k, v in SCAN[1].items()} | dict(dA=None, dB=None, dC=None))
+    _, fin = ag.selective_scan(x, x.detach(), A, B, B)
+    torch.cat([torch.zeros(3), fin.reshape(-1)]).mul(torch.arange(27.0)).sum().backward()
+    (dfinal,) = seen
+    assert dfinal.is_contiguous() and dfinal.data_ptr() % 16 == 0
+    assert torch.equal(dfinal.reshape(-1), torch.arange(3.0, 27.0))

@@ -76,3 +76,16 @@ def test_a_saved_state_is_too_new_after_a_step():
         graph.replay()
         want = layers.short_conv_step(x, want_state, w)
         assert torch.equal(out, want) and torch.equal(graph_state, want_state)
+
+
+def test_gradient_of_a_final_state_inside_a_larger_one():
+    v, d = scan_inputs(101, F32, 2, 40, 32, 16, 2, 2, "softplus dt_bias gate skip state")
+    c = d(3 + 2 * 32 * 16)[0]
+    got = []
+    for joined in (False, True):
+        leaves = {k: t[0].clone().requires_grad_() for k, t in v.items()}
+        _, fin = ag.selective_scan(**leaves, dt_softplus=True)
+        flat = torch.cat([c[:3], fin.reshape(-1)]) * c if joined else fin.reshape(-1) * c[3:].clone()
+        got.append(torch.autograd.grad(flat.sum(), list(leaves.values()), allow_unused=True))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
