@@ -3,9 +3,11 @@ a scale changed in place, states that a graph has saved."""
 import pytest
 import torch
 
+import chunked_gated_delta_09_amd as kda
 from chunked_gated_delta_09_amd import autograd as ag
 from chunked_gated_delta_09_amd import layers
-from tests.test_gpu_layers import Draw, F32, scan_inputs
+from tests import layer_ref as ref
+from tests.test_gpu_layers import BF16, F32, Draw, ops, scan_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +91,73 @@ def test_gradient_of_a_final_state_inside_a_larger_one():
         got.append(torch.autograd.grad(flat.sum(), list(leaves.values()), allow_unused=True))
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def shifted(t, by):
+    """The values of t, contiguous, beginning `by` elements behind an aligned address."""
+    if t is None or not t.numel():
+        return t
+    out = t.new_empty(t.numel() + by)[by:].view(t.shape)
+    out.copy_(t)
+    assert out.data_ptr() % 16 == by * t.element_size() % 16
+    return out
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("by", [1, 2, 3])
+def test_tensors_that_begin_anywhere(dtype, by):
+    """Widths that allow wide loads, addresses that do not: the values of aligned tensors' calls."""
+    d = Draw(103)
+    B, T, D, NS, W = 2, 37, 64, 16, 4
+    x, dt, z, dy = (d(B, T, D, dtype=dtype)[0] for _ in range(4))
+    Bm, Cm = (d(B, T, 1, NS, dtype=dtype)[0] for _ in range(2))
+    w, bias, wn = d(D, W)[0], d(D)[0], d(16)[0]
+    hc, h0, A = d(B, W - 1, D, dtype=dtype)[0], d(B, D, NS)[0], -torch.rand(D, NS, generator=d.g).cuda()
+    q, v = d(B, 2, 32, dtype=dtype)[0], d(B, 2, 32, dtype=dtype)[0]
+    g, beta, S = -torch.rand(B, 2, 32, generator=d.g).cuda(), torch.rand(B, 2, generator=d.g).cuda(), d(B, 2, 32, 32)[0]
+
+    def run(m):
+        out = []
+        f = layers.short_conv(m(x), m(w), bias=m(bias), h0=m(hc), output_final_state=True)
+        r = layers.short_conv_bwd(m(x), m(w), m(dy), bias=m(bias), h0=m(hc), dfinal=m(hc))
+        out += [f["y"], f["final_state"], r["dx"], r["dweight"], r["dbias"], r["dh0"]]
+        f = layers.selective_scan(m(x), m(dt), A, m(Bm), m(Cm), skip=m(bias), z=m(z), dt_bias=m(bias), h0=h0, dt_softplus=True,
+                                  save=True)
+        r = layers.selective_scan_bwd(m(x), m(dt), A, m(Bm), m(Cm), f["states"], m(dy), skip=m(bias), z=m(z), dt_bias=m(bias),
+                                      dt_softplus=True)
+        out += [f["y"], f["final_state"]] + [r[k] for k in ("dx", "ddt", "dA", "dB", "dC", "dskip", "dz", "ddt_bias")]
+        kw = dict(weight=m(wn), bias=m(wn), gate=m(z), activation="silu", center=True)
+        r = layers.group_norm_bwd(m(x), 4, m(dy), **kw)
+        out += [layers.group_norm(m(x), 4, **kw), r["dx"], r["dweight"], r["dbias"], r["dgate"]]
+        state = m(hc).clone() if m is not shifted_by else shifted_by(hc)
+        out += [layers.short_conv_step(m(x[:, 0].contiguous()), state, m(w), bias=m(bias)), state]
+        st = h0.clone()
+        out += [layers.selective_scan_step(m(x[:, 0].contiguous()), m(dt[:, 0].contiguous()), A, m(Bm[:, 0].contiguous()),
+                                           m(Cm[:, 0].contiguous()), st, z=m(z[:, 0].contiguous()), dt_softplus=True), st]
+        Sk = S.clone() if m is not shifted_by else shifted_by(S)
+        out += [layers.kda_step(m(q), m(q), m(v), m(g), m(beta), Sk), Sk]
+        return out
+
+    def shifted_by(t):
+        return shifted(t, by)
+
+    for i, (a, b) in enumerate(zip(run(lambda t: t), run(shifted_by))):
+        assert a.shape == b.shape
+        ref.close(b, a.cpu(), a.dtype, ops(T), i)
+
+
+def test_scan_states_that_begin_anywhere_are_refused():
+    """Rows of 16 states are read whole: the call says so rather than reading across."""
+    d = Draw(105)
+    x, A, b = d(1, 8, 8)[0], -torch.ones(8, 16, device="cuda"), d(1, 8, 1, 16)[0]
+    with pytest.raises(kda.KdaError, match="h0 must be 16-byte aligned"):
+        layers.selective_scan(x, x, A, b, b, h0=shifted(d(1, 8, 16)[0], 1))
+    with pytest.raises(kda.KdaError, match="A must be 16-byte aligned"):
+        layers.selective_scan(x, x, shifted(A, 1), b, b)
+    with pytest.raises(kda.KdaError, match="state must be 16-byte aligned"):
+        layers.selective_scan_step(x[0], x[0], A, b[0], b[0], shifted(d(8, 8, 16)[0], 1))
+    odd = [shifted(t, 1) for t in (-torch.rand(8, 13, generator=d.g).cuda(), d(1, 8, 13)[0])]  # 13 states: single loads
+    c = d(1, 8, 1, 13)[0]
+    f = layers.selective_scan(x, x, odd[0], c, c, h0=odd[1])
+    want = layers.selective_scan(x, x, odd[0].clone(), c, c, h0=odd[1].clone())
+    assert torch.equal(f["y"], want["y"]) and torch.equal(f["final_state"], want["final_state"])
