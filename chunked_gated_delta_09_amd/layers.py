@@ -105,11 +105,9 @@ def _launch(dev, fn, *args):
         _check(status)
 
 
-def _step(dev, fn, state, *args):
-    """_launch for a call that writes `state`. Torch does not see a write through an address: the tensor's version is
-    counted up by hand, so that a graph which has saved it refuses its backward."""
-    _launch(dev, fn, *args)
-    torch._C._increment_version((state,))
+# Torch does not see a write through an address: a step counts its state's version up by hand, so that a graph which
+# has saved the state refuses its backward.
+_written = torch._C._increment_version
 
 
 def _refuse(t, name, dtype, shape, dev):
@@ -334,7 +332,8 @@ def short_conv_step(x, state, weight, bias=None, slots=None, activation="silu"):
     psl = _need(slots, "slots", torch.int32, (B,), dev)
     plan = _plan(_ConvDims, B, 1, D, W, B, None, None, row, _act(activation, (None, "silu")), _DT[x.dtype])
     y, py = _like(x, row)
-    _step(dev, _lib().kda_short_conv_step, state, plan.ref, px, pw, pb, psl, _fit("S", S), pst, py)
+    _launch(dev, _lib().kda_short_conv_step, plan.ref, px, pw, pb, psl, S if S <= _I32_MAX else _fit("S", S), pst, py)
+    _written((state,))
     return y
 
 
@@ -424,7 +423,8 @@ def selective_scan_step(x, dt, A, B, C, state, slots=None, skip=None, z=None, dt
     pst = _need(state, "state", F32, (S, D, NS), dev)
     psl = _need(slots, "slots", torch.int32, rows, dev)
     y, py = _like(x, strides[0])
-    _step(dev, _lib().kda_sscan_step, state, plan.ref, *ptrs, psl, _fit("S", S), pst, py)
+    _launch(dev, _lib().kda_sscan_step, plan.ref, *ptrs, psl, S if S <= _I32_MAX else _fit("S", S), pst, py)
+    _written((state,))
     return y
 
 
@@ -490,5 +490,6 @@ def kda_step(q, k, v, g, beta, state, slots=None, scale=None, beta_logits=False)
     scale = None if scale is None else float(scale)
     _, d = _kda_dims(B, H, HV, K, V, scale, "f32" if dt is F32 else "bf16", bool(beta_logits))
     o, po = _like(v)
-    _step(dev, _lib().kda_step, state, d, *ptrs, _fit("S", S), pst, po)
+    _launch(dev, _lib().kda_step, d, *ptrs, S if S <= _I32_MAX else _fit("S", S), pst, po)
+    _written((state,))
     return o
