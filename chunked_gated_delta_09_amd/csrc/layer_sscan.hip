@@ -128,19 +128,32 @@ __device__ __forceinline__ void store_states(float* p, int64_t row, int N, int p
     if (part * NPL + i < N) p[row * N + part * NPL + i] = v[i];
 }
 
+__device__ __forceinline__ void unpack(const float4& v, float (&out)[4]) {
+  out[0] = v.x;
+  out[1] = v.y;
+  out[2] = v.z;
+  out[3] = v.w;
+}
+
 // h 2^e, for e of any size: over a segment 2^e alone can be past fp32 where the product is not, and is zero where h
-// is. The fraction's factor is in (1/2, 1], the rest goes into the exponent. (A NaN in e is one in what the
-// segment adds, too.)
+// is. The fraction's factor is in (1/2, 1], the rest goes into the exponent; a NaN stays one.
 __device__ __forceinline__ float times_exp2(float h, float e) {
-  const float low = fmaxf(e, -1024.f), whole = ceilf(low);
+  const float low = e < -1024.f ? -1024.f : e, whole = ceilf(low);
   return ldexpf(h * exp2_hw(low - whole), (int)whole);
 }
 
 // Carries h through `count` segments from `s` on (step: the one behind or before): h <- exp(A sum dt) h +
-// loc. Eight segments are loaded together, since only the sums depend on each other.
+// loc. Eight segments are loaded together, since only the sums depend on each other. The factors are at most one where dt
+// comes from a softplus and no A of the wave is above zero; otherwise eight with a factor that may be past fp32 are
+// taken one by one, each product formed by its exponent (for all calls that took 1 % of B=1, T=16384, D=2048, N=16:
+// 240 against 238 us).
 template <int NP>
 __device__ __forceinline__ void join_segments(const ScanArgs& a, int64_t s, int step, int64_t count, int64_t d, int part,
                                               const float (&A2)[NPL], float (&h)[NPL]) {
+  bool up = a.softplus == 0;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) up = up || A2[i] > 0.f;
+  const bool may_grow = __any(up);
   for (int64_t k = 0; k < count; k += 8) {
     float sum[8];
     float4 loc[8];
@@ -151,12 +164,30 @@ __device__ __forceinline__ void join_segments(const ScanArgs& a, int64_t s, int 
         sum[u] = a.seg_dt[row];
         loc[u] = *reinterpret_cast<const float4*>(a.seg_state + row * NP + part * NPL);
       }
+    if (may_grow) {
+      bool past = false;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) past = past || (k + u < count && sum[u] * A2[i] > 126.f);
+      if (__any(past)) {
+#pragma unroll 1
+        for (int64_t v = k; v < min(k + 8, count); ++v) {
+          const int64_t row = (s + (int64_t)step * v) * a.D + d;
+          float add[NPL];
+          unpack(*reinterpret_cast<const float4*>(a.seg_state + row * NP + part * NPL), add);
+#pragma unroll
+          for (int i = 0; i < NPL; ++i) h[i] = times_exp2(h[i], a.seg_dt[row] * A2[i]) + add[i];
+        }
+        continue;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < 8; ++u)
       if (k + u < count) {
         const float add[NPL] = {loc[u].x, loc[u].y, loc[u].z, loc[u].w};
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) h[i] = times_exp2(h[i], sum[u] * A2[i]) + add[i];
+        for (int i = 0; i < NPL; ++i) h[i] = fmaf(exp2_hw(sum[u] * A2[i]), h[i], add[i]);
       }
   }
 }
@@ -222,13 +253,6 @@ struct Stage {
     if (tid < L::CH) to[tid] = p != nullptr && c0 + tid < per ? p[(int64_t)grp * per + c0 + tid] : 0.f;
   }
 };
-
-__device__ __forceinline__ void unpack(const float4& v, float (&out)[4]) {
-  out[0] = v.x;
-  out[1] = v.y;
-  out[2] = v.z;
-  out[3] = v.w;
-}
 
 // dt of four channels from the raw steps; zero for a token that is not there, which leaves states as
 // they are.

@@ -114,3 +114,19 @@ def test_selective_scan_one_state_and_a_bias(dtype, seqs):
              A=(A.cuda(), A.to(ref.F64).requires_grad_()), B=d(B, T, G, NS, dtype=dtype), C=d(B, T, G, NS, dtype=dtype),
              skip=none, z=none, dt_bias=(bias.cuda(), bias.to(ref.F64).requires_grad_()), h0=d(N, D, NS))
     check_scan(v, d(B, T, D, dtype=dtype, leaf=False), d(N, D, NS, leaf=False), dtype, cu, False)
+
+
+def test_selective_scan_growth_of_little():
+    """16 tokens, one segment, that multiply a state of 1e-36 by e^96: the factor is past fp32, the product is not."""
+    T, D, NS = 200, 8, 8
+    d = Draw(89)
+    assert scan_plan([T], D, NS, 1, False)[:2] == (16, 16)
+    dt = torch.zeros(1, T, D)
+    dt[:, 16:32] = -6.0
+    host = dict(x=torch.zeros(1, T, D), dt=dt, A=torch.full((D, NS), -1.0), B=torch.randn(1, T, 1, NS, generator=d.g),
+                C=torch.randn(1, T, 1, NS, generator=d.g))
+    h0 = torch.randn(1, D, NS, generator=d.g) * 1e-36
+    f = layers.selective_scan(**{k: v.cuda() for k, v in host.items()}, h0=h0.cuda())
+    y64, f64 = ref.scan(*(v.to(ref.F64) for v in host.values()), None, None, None, h0.to(ref.F64), False, None)
+    ref.close(f["y"], y64, F32, ops(T), "y")
+    ref.close(f["final_state"], f64, F32, ops(T), "final_state")
