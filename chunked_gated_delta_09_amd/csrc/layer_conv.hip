@@ -2,8 +2,8 @@
 //
 // A thread owns VEC neighbouring channels and walks a run of tokens with the last W - 1 inputs in
 // registers, so every input is loaded once per run plus W - 1 rows in front of it. The work is
-// bound by memory: on B=4, T=4096, D=4096, W=4 in bf16 the forward moves its 268 MB in 50 us (5.3 TB/s, the
-// rate of a large copy), the backward its 403 MB in 92 us (4.4 TB/s).
+// bound by memory: on B=4, T=4096, D=4096, W=4 in bf16 the forward moves its 268 MB in 54 us (5.0 TB/s; a large
+// copy 5.2), the backward its 403 MB in 92 us (4.4 TB/s).
 #include "layer_device.h"
 
 namespace kda {
@@ -443,7 +443,7 @@ hipError_t fwd_w(const ConvArgs& a, hipStream_t st) {
 
 template <class T, int W>
 hipError_t bwd_w(const ConvArgs& a, hipStream_t st) {
-  // two channels a thread (94 registers, five waves a SIMD) took 92 us where four (180) took 99 on B=4,
+  // two channels a thread (96 registers, five waves a SIMD) take 92 us where four (two waves) take 97 on B=4,
   // T=4096, D=4096, W=4
   const int vec = a.vec > 1 ? 2 : 1;
   const int64_t rb = conv_row_blocks(a);
@@ -488,8 +488,8 @@ hipError_t step_w(const ConvStepArgs& a, hipStream_t st) {
 }  // namespace
 
 // Channels of a thread: four where every row starts on a multiple of them, single ones otherwise.
-// (Eight bf16 channels, 16 bytes a load, took 64 us where four take 56 on B=4, T=4096, D=4096, W=4:
-// filter, window and rows ahead of eight channels leave three waves a SIMD instead of six.)
+// (Eight bf16 channels, 16 bytes a load, take 56 us where four take 54 on B=4, T=4096, D=4096, W=4: filter,
+// window and rows ahead of eight channels leave fewer waves a SIMD.)
 int conv_vec(int dtype, int D, int64_t x_row, const void* const* ptrs, int np) {
   const int es = dtype == KDA_F32 ? 4 : 2;
   bool ok = D % 4 == 0 && x_row % 4 == 0;
@@ -499,7 +499,7 @@ int conv_vec(int dtype, int D, int64_t x_row, const void* const* ptrs, int np) {
 
 // Tokens of a run: as many as leave about 2048 waves, from 8 to 64 (a longer run reads its W - 1
 // rows in front less often, a shorter one gives more waves to a small call). 64 against 32 on
-// B=4, T=4096, D=4096: forward 50 against 56 us, backward 99 against 116.
+// B=4, T=4096, D=4096: forward 54 against 60 us, backward 92 against 98.
 int conv_tile(int64_t total, int D, int vec) {
   const int64_t cols = (D + vec - 1) / vec;
   int tt = 64;

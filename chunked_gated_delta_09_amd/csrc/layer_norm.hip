@@ -3,8 +3,8 @@
 // A group's C channels are held in registers by tpi lanes (a power of two up to a wave, or a whole
 // workgroup of 256 or 1024), one or two chunks of 16 bytes each, so a row is read once: the mean, the
 // centred sum of squares and the output come from the registers. Bound by memory: 16384 rows of 32 x 128,
-// bf16, gated, move their 403 MB forward in 78 us (5.2 TB/s, the rate of a large copy) and their 671 MB
-// backward in 127 (5.3).
+// bf16, gated, move their 403 MB forward in 81 us (5.0 TB/s; a large copy 5.2) and their 671 MB backward in
+// 128 (5.2).
 #include "layer_device.h"
 
 namespace kda {
@@ -32,7 +32,7 @@ __device__ __forceinline__ float item_sum(float x, int tpi, float* sh) {
 // Where a lane's elements are in its group. NEAR (C a multiple of VEC): VEC neighbours a chunk, loaded
 // together where rows are aligned for it (`vec`). Otherwise neighbouring lanes have neighbouring
 // elements, so that loads and stores of single elements cover whole lines (1500 rows of 3 x 333, fp32:
-// 7 against 10 us). The choice goes by C alone: the order of a group's sums, and with it its bits, does
+// forward 6.7 against 10.4 us, backward 13.8 against 17.5). The choice goes by C alone: the order of a group's sums, and with it its bits, does
 // not depend on where the tensor lies.
 template <int VEC, bool NEAR>
 struct Place {

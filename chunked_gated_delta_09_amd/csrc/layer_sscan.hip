@@ -6,9 +6,11 @@
 // dt and dt x by the lanes that loaded them, and passed through shared memory; the recurrence
 // itself stays in registers. The work is bound by the vector unit: a state and token takes five
 // instructions (dt A, its exponential at half rate, dt x B, two multiply-adds), a channel and token
-// about 30 more shared by its lanes. Measured, bf16, N = 16: B=1, T=16384, D=2048 takes 109 us for the first
-// pass and 159 for the second, with the vector unit busy 85 and 87 % of the time; B=2, T=2048, D=2048 takes 31
-// and 46 us, its backward 32 (local pass), 145 (72 % busy, two waves a SIMD) and 5 (sums).
+// about 30 more shared by its lanes. Measured, bf16, N = 16, calls back to back: B=1, T=16384, D=2048 takes 96 us
+// for the first pass and 139 for the second, with the vector unit issuing 82 and 85 % of the time; B=2, T=2048,
+// D=2048 takes 28 and 42 us (59 and 66 %), its backward 30 (local pass, 57 %), 131 (71 %, two waves a SIMD) and 5
+// (sums). A chip that was idle has a lower clock for its first 20 ms, and the same kernels take 10 to 20 % longer
+// (112, 162; 31, 46, 33, 146 us); the variants named here and below were compared there.
 // Staging through two buffers with one barrier a chunk took 175 us for the 165 of that time's second
 // pass. All states of a channel in one lane would save the joins over lanes, and leave a quarter of the
 // waves; sixteen lanes a channel would cost four joins a state.
@@ -1034,7 +1036,7 @@ hipError_t bwd_np(const ScanArgs& a, hipStream_t st) {
 }
 
 // Two tiles of channels a workgroup where that still gives two workgroups a CU, one otherwise (128 sequences,
-// D = 4096, N = 16: 24.5, 19.1, 23.4 us with one, two, four).
+// D = 4096, N = 16: 24.4, 19.5, 23.2 us with one, two, four).
 template <class T, int NP>
 hipError_t step_np(const ScanStepArgs& a, hipStream_t st) {
   const int ch = Lanes<NP>::CH, per = a.D / a.G, wide = (per + 2 * ch - 1) / (2 * ch);
@@ -1075,9 +1077,9 @@ int scan_tiles(int D, int N, int G) {
 // two (backward, whose registers allow no more), and where the longest sequence is at most two such
 // segments not at all: the pass that a cut needs costs more than the fuller grid gives. A call that
 // leaves the chip idle either way is cut for its latency: a chunk takes a workgroup alone 4 us (forward) or
-// 8 (backward), a local segment joined on entry about 0.08, which balances near a quarter of the
-// square root of the length in chunks. Local segments: shorter by up to four while that keeps the first
-// pass within eight workgroups a CU and the joins few.
+// 8 (backward), a local segment joined on entry about 0.08, which balances at a seventh (a tenth) of the
+// square root of the length in chunks; a ninth is taken for both. Local segments: shorter by up to four while that
+// keeps the first pass within eight workgroups a CU and the joins few.
 void scan_seg(const Seqs& s, int64_t longest, int D, int N, int G, bool bwd, int* seg, int* lseg) {
   const int64_t cols = (int64_t)G * scan_tiles(D, N, G), C = kScanChunk;
   const int64_t whole = longest > 0 ? (longest + C - 1) / C * C : C;

@@ -3,9 +3,9 @@
 // A workgroup holds a tile of columns of one head's state in registers (rows dealt to groups of lanes,
 // four columns a lane), so the state is read once and written once: k^T S', q^T S' and q.k are summed
 // together, u = beta (v - k^T S') follows, and o = scale (q^T S' + (q.k) u). Bound by the state's bytes:
-// 256 sequences of 32 heads of 128 x 128 take 207 us for their 1.07 GB (5.2 TB/s, the rate of a large
-// copy). Tiles of 32 columns: 64 or 128 columns a workgroup (longer pieces of a row, fewer workgroups)
-// took 205 and 308 us there, and leave fewer workgroups to a small call.
+// 256 sequences of 32 heads of 128 x 128 take 210 us for their 1.07 GB (5.1 TB/s; a large copy
+// 5.2). Tiles of 32 columns: 64 or 128 columns a workgroup (longer pieces of a row, fewer workgroups) took 205 and
+// 308 us where these took 207, and leave fewer workgroups to a small call.
 #include "layer_device.h"
 
 namespace kda {

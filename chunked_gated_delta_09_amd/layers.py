@@ -10,7 +10,8 @@ on a multiple of 16 bytes, as tensors of their own do.
 
 Packed sequences: ``cu_seqlens`` is the host list of cuts, with batch size 1; a caller that has a
 device copy (int32) passes it as ``cu_seqlens_dev``, otherwise the call makes one (which copies
-from the host, so it cannot be captured into a graph).
+from the host, so it cannot be captured into a graph). Both hold the same cuts for as long as the call, or a
+graph that has captured it, runs.
 
 Token steps update the state in place. ``slots`` (int32 [B] on the GPU) names the state row of each
 batch row; None: row b. A negative slot marks a padding row (no state is touched, its output is

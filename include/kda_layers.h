@@ -8,7 +8,8 @@
  * of the current HIP device with no allocation, no synchronisation and no state kept between
  * calls; arguments checked before any HIP call (KDA_EINVAL / KDA_EUNSUPPORTED with a message
  * from kda_last_error()); sums in fp32 in a fixed order, so results are the same from run to run.
- * Every call may be captured into a HIP graph.
+ * Every call may be captured into a HIP graph; sizes and cuts are those of the capture, and the device
+ * copy of the cuts still holds them at every replay.
  *
  * Token axis: dense batches are [B, T, ...]; packed sequences have B = 1, T tokens in all and
  * cu_seqlens (device and host copies with the same values) with N sequences, empty ones allowed.
