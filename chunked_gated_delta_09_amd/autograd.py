@@ -118,11 +118,12 @@ class SelectiveScanFunction(torch.autograd.Function):
     """y, final_state = selective_scan(x, dt, A, B, C, skip, z, dt_bias, h0) with gradients for all nine."""
 
     @staticmethod
-    def forward(ctx, x, dt, A, B, C, skip, z, dt_bias, h0, cu_seqlens, cu_seqlens_dev, dt_softplus, output_final_state):
+    def forward(ctx, x, dt, A, B, C, skip, z, dt_bias, h0, cu_seqlens, cu_seqlens_dev, dt_softplus, output_final_state,
+                save=True):
         cu_seqlens, cu_seqlens_dev = _kept_both(cu_seqlens, cu_seqlens_dev, x.device)
         f = layers.selective_scan(x, dt, A, B, C, skip=skip, z=z, dt_bias=dt_bias, h0=h0, cu_seqlens=cu_seqlens,
                                   cu_seqlens_dev=cu_seqlens_dev, dt_softplus=dt_softplus,
-                                  output_final_state=output_final_state, save=True)
+                                  output_final_state=output_final_state, save=save)
         ctx.save_for_backward(x, dt, A, B, C, skip, z, dt_bias, cu_seqlens_dev, f["states"])
         ctx.cu_seqlens, ctx.dt_softplus, ctx.has_h0 = cu_seqlens, dt_softplus, h0 is not None
         ctx.set_materialize_grads(False)
@@ -137,20 +138,17 @@ class SelectiveScanFunction(torch.autograd.Function):
                                       dfinal=_rows16(dfinal), cu_seqlens=ctx.cu_seqlens,
                                       cu_seqlens_dev=cu_dev, dt_softplus=ctx.dt_softplus, output_dh0=ctx.has_h0)
         return (r["dx"], r["ddt"], r["dA"], r["dB"], r["dC"], r["dskip"], r["dz"], r["ddt_bias"], r["dh0"], None, None,
-                None, None)
+                None, None, None)
 
 
 def selective_scan(x, dt, A, B, C, skip=None, z=None, dt_bias=None, h0=None, cu_seqlens=None, cu_seqlens_dev=None,
                    dt_softplus=False, output_final_state=True):
     """Differentiable ``layers.selective_scan``. Returns (y, final_state or None). The states of the chunks are
     kept (and written) where a backward can follow."""
-    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, dt, A, B, C, skip, z, dt_bias, h0))):
-        f = layers.selective_scan(x, dt, A, B, C, skip=skip, z=z, dt_bias=dt_bias, h0=h0, cu_seqlens=cu_seqlens,
-                                  cu_seqlens_dev=cu_seqlens_dev, dt_softplus=dt_softplus,
-                                  output_final_state=output_final_state, save=False)
-        return f["y"], f["final_state"]
+    save = torch.is_grad_enabled() and any(t is not None and t.requires_grad
+                                           for t in (x, dt, A, B, C, skip, z, dt_bias, h0))
     return SelectiveScanFunction.apply(x, dt, A, B, C, skip, z, dt_bias, h0, cu_seqlens, cu_seqlens_dev, dt_softplus,
-                                       output_final_state)
+                                       output_final_state, save)
 
 
 class GroupNormFunction(torch.autograd.Function):

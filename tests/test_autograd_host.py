@@ -137,3 +137,13 @@ def test_selective_scan_backward_aligns_the_final_states_gradient(monkeypatch):
     (dfinal,) = seen
     assert dfinal.is_contiguous() and dfinal.data_ptr() % 16 == 0
     assert torch.equal(dfinal.reshape(-1), torch.arange(3.0, 27.0))
+
+
+def test_selective_scan_refuses_forward_mode(monkeypatch):
+    """It has no forward-mode derivative: dual numbers raise rather than lose their tangents."""
+    record(monkeypatch, ag.layers, ("selective_scan", "selective_scan_bwd"), SCAN)
+    x, A, B = torch.zeros(1, 5, 3), torch.zeros(3, 2), torch.zeros(1, 5, 1, 2)
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual(x, torch.ones_like(x))
+        with pytest.raises((NotImplementedError, RuntimeError), match="jvp"):
+            ag.selective_scan(dual, x, A, B, B)
