@@ -49,18 +49,26 @@ def _fit(name, v):
     return v
 
 
-class _ConvDims(ctypes.Structure):
+class _Dims(ctypes.Structure):
+    """A size structure and the binding that declares its queries: an undeclared one's answer is cut to 32 bits."""
+
+    @staticmethod
+    def library():
+        return _lib()
+
+
+class _ConvDims(_Dims):
     _fields_ = [("B", _i32), ("T", _i32), ("D", _i32), ("W", _i32), ("N", _i32), ("cu_seqlens_dev", _vp),
                 ("cu_seqlens_host", _pi32), ("x_row", _i64), ("act", _i32), ("dtype", _i32)]
 
 
-class _ScanDims(ctypes.Structure):
+class _ScanDims(_Dims):
     _fields_ = [("B", _i32), ("T", _i32), ("D", _i32), ("NS", _i32), ("G", _i32), ("N", _i32), ("cu_seqlens_dev", _vp),
                 ("cu_seqlens_host", _pi32), ("x_row", _i64), ("dt_row", _i64), ("z_row", _i64), ("b_row", _i64),
                 ("c_row", _i64), ("softplus", _i32), ("dtype", _i32)]
 
 
-class _NormDims(ctypes.Structure):
+class _NormDims(_Dims):
     _fields_ = [("R", _i64), ("G", _i32), ("C", _i32), ("center", _i32), ("act", _i32), ("shared", _i32), ("eps", _f32),
                 ("x_row", _i64), ("gate_row", _i64), ("dtype", _i32)]
 
@@ -206,7 +214,7 @@ class _Plan:
     def size(self, query):
         n = self.sizes.get(query)
         if n is None:
-            n = getattr(_lib(), query)(self.ref)
+            n = getattr(self.dims.library(), query)(self.ref)
             if n > 0:
                 self.sizes[query] = n
         return n

@@ -24,13 +24,19 @@ __all__ = ["linear_attention", "linear_attention_bwd", "linear_attention_step", 
 F32 = torch.float32
 
 
-class _LinDims(ctypes.Structure):
+class _Dims(ctypes.Structure):
+    @staticmethod
+    def library():
+        return _lib()
+
+
+class _LinDims(_Dims):
     _fields_ = [("B", _i32), ("T", _i32), ("H", _i32), ("HV", _i32), ("K", _i32), ("V", _i32), ("N", _i32),
                 ("cu_seqlens_dev", _vp), ("cu_seqlens_host", _pi32), ("q_row", _i64), ("k_row", _i64), ("v_row", _i64),
                 ("g_const", _i32), ("scale", _f32), ("dtype", _i32)]
 
 
-class _WinDims(ctypes.Structure):
+class _WinDims(_Dims):
     _fields_ = [("B", _i32), ("T", _i32), ("H", _i32), ("HK", _i32), ("D", _i32), ("N", _i32), ("cu_seqlens_dev", _vp),
                 ("cu_seqlens_host", _pi32), ("q_row", _i64), ("k_row", _i64), ("v_row", _i64), ("window", _i32),
                 ("sinks", _i32), ("scale", _f32), ("dtype", _i32)]

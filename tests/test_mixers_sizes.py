@@ -1,0 +1,28 @@
+"""Sizes and limits of the token mixers' calls, as the library answers them (no GPU)."""
+import subprocess
+import sys
+
+import pytest
+
+FIRST_QUERY = """
+import ctypes
+from chunked_gated_delta_09_amd import layers, mixers
+cu = list(range(2200)) + [30000]
+host = (ctypes.c_int32 * len(cu))(*cu)
+if {lin}:
+    plan = layers._plan_of(mixers._LinDims, 256, host, (1, cu[-1], 32, 32, 128, 128, len(cu) - 1), (0, 0, 0, 0, 1.0, 1))
+else:
+    plan = layers._plan_of(mixers._WinDims, None, None, (1, 1 << 22, 255, 1, 256, 1), (0, 0, 0, 8, 1024, 1.0, 1))
+print(plan.size("{query}"))
+"""
+
+
+@pytest.mark.parametrize("lin,query", [(True, "kda_lattn_fwd_workspace_bytes"), (True, "kda_lattn_bwd_workspace_bytes"),
+                                       (False, "kda_wattn_bwd_workspace_bytes")])
+def test_the_first_query_of_a_process_answers_past_32_bits(lin, query):
+    """Nothing has declared the library's functions yet when a plan asks for a size."""
+    r = subprocess.run([sys.executable, "-c", FIRST_QUERY.format(lin=lin, query=query)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    # a state of every sequence's; do.o of every row and one part of the queries at the least
+    least = 2200 * 32 * 128 * 128 * 4 if lin else (1 << 22) * 255 * 4 + 1024 * 2 * 256 * 4 * 10
+    assert int(r.stdout) >= least > 1 << 32
