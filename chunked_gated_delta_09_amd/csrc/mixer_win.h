@@ -641,7 +641,9 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void 
         }
       }
       const Frag<T> pf = to_frag<T>(stack(s[0], s[1])), sf = to_frag<T>(stack(dp[0], dp[1]));
-      const bool careful = again.value && !(q0 >= k0 + 15 && q0 + 31 - k0 < a.window);
+      // a first token's key may come behind a query that is behind the window (more first tokens than the window has): such
+      // blocks are few, and formed without what is not finite at once
+      const bool careful = NEAR ? again.value && !(q0 >= k0 + 15 && q0 + 31 - k0 < a.window) : q0 < k0 + 15;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
         Frag<T> df = L::col(td, 0, dt * 16), qf = L::col(tq, 0, dt * 16);
@@ -655,7 +657,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void 
       if (careful) {
         auto seen = [&](int, int r) {
           const int qi = q0 + r, j = k0 + l16;
-          return j <= qi && qi - j < a.window;
+          return NEAR ? j <= qi && qi - j < a.window : qi - j >= a.window;
         };
         add_not_finite<T, DP>(td, 32, dv, seen);
         add_not_finite<T, DP>(tq, 32, dk, seen);
@@ -670,7 +672,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void 
       return false;
     }
   };
-  // the first tokens' queries behind the window all see them
+  // of a pair that a part leaves out, but for those blocks, the query sees the key through the window
   if (pass(std::false_type())) pass(std::true_type());
   // the waves' sums, in order
   constexpr int LO = 2 * DP + 4;
