@@ -8,7 +8,9 @@
 //   dk_j = e^{whole - G_j} v_j dS^T + sum_{i >= j} scale e^{G_i - G_j} (do_i.v_j) q_i,   dS <- e^{whole} dS + sum_i scale e^{G_i} q_i do_i^T.
 // So one kernel does all four: out_i = in_i (x_i S) + sum_j pair_ij (x_i.y_j) z_j, S <- decay S + sum_j up_j y_j z_j^T.
 // The decays are differences of G, never quotients of exponentials, so no gate is too strong; G is summed in 64 bits and
-// held as two fp32 numbers, so that a strong gate among weak ones costs them nothing.
+// held as two fp32 numbers, so that a strong gate among weak ones costs them nothing. A gate that is not finite (-infinity is the
+// lowest of the finite ones) would make NaN of differences that do not cross it: it is left out of G, and a chunk's set of such
+// tokens says which decays are NaN.
 //
 // A workgroup has one head's state for a tile of its columns: each of its waves holds [P, 16] in matrix results. Per chunk the
 // waves share the pairs out among them (they go through shared memory, for all columns need them), then each forms its columns of
@@ -50,6 +52,8 @@ __global__ __launch_bounds__(64 * NW, PP <= 128 ? NW / 2 : NW / 4) void lin_walk
   constexpr int LX = PP + kPadCol<T>, LY = PP + kPadCol<T>, LZ = RB + kPadCol<T>, LP = CH + kPad<T>, LW = RB + kPadCol<T>;
   __shared__ __align__(16) T sx[OUT ? CH * LX : 8], sy[CH * LY], sz[CH * LZ], sw[DOT ? CH * LW : 8], sp_[OUT ? CH * LP : 8];
   __shared__ float sg[kGateChunks][4][CH];  // G in two parts, scale e^G, e^(whole - G)
+  __shared__ float sdec[kGateChunks], sw_[OUT ? 1 : kGateChunks][2];  // e^whole; whole in two parts
+  __shared__ uint32_t sbad[OUT ? kGateChunks : 1];  // a bit for each token whose gate is not finite
   __shared__ float red[DOT ? NW : 1][DOT ? CH : 1];
   __shared__ float sm[DOT && !REV ? IT * IT : 1][2][16];  // sums of M over a tile's earlier and later tokens
 
@@ -132,18 +136,31 @@ __global__ __launch_bounds__(64 * NW, PP <= 128 ? NW / 2 : NW / 4) void lin_walk
       int g_lane = lane;
       asm volatile("" : "+v"(g_lane));  // as in Stage
       const int k = wave * GPER + g_lane / CH;
-      double v = (gt < -1e4f ? -1e4 : (double)gt) * 1.4426950408889634;
+      static_assert(CH == 32);
+      const bool odd = !(gt < INFINITY);
+      const int i = g_lane % CH;
+      const uint32_t bad = (uint32_t)(__ballot(odd) >> (g_lane - i));
+      double v = (odd ? 0.0 : gt < -1e4f ? -1e4 : (double)gt) * 1.4426950408889634;
 #pragma unroll
       for (int d = 1; d < CH; d *= 2) {
         const double o = __shfl_up(v, d, CH);
-        if (g_lane % CH >= d) v += o;
+        if (i >= d) v += o;
       }
       const float hi = (float)v, rest = (float)(__shfl(v, CH - 1, CH) - v);
       if (k < kGateChunks) {
-        sg[k][0][g_lane % CH] = hi;
-        sg[k][1][g_lane % CH] = (float)(v - (double)hi);
-        sg[k][2][g_lane % CH] = a.scale * exp2_hw(hi);
-        sg[k][3][g_lane % CH] = exp2_hw(rest);
+        sg[k][0][i] = hi;
+        sg[k][1][i] = (float)(v - (double)hi);
+        sg[k][2][i] = bad << (CH - 1 - i) ? __builtin_nanf("") : a.scale * exp2_hw(hi);
+        sg[k][3][i] = bad >> i >> 1 ? __builtin_nanf("") : exp2_hw(rest);
+        if (i == CH - 1) {
+          if constexpr (OUT) {
+            sbad[k] = bad;
+          } else {
+            sw_[k][0] = bad ? __builtin_nanf("") : hi;
+            sw_[k][1] = (float)(v - (double)hi);
+          }
+          sdec[k] = bad ? __builtin_nanf("") : exp2_hw(hi);
+        }
       }
     }
     if constexpr (OUT) fx.store_stacked(sx, LX);
@@ -157,7 +174,7 @@ __global__ __launch_bounds__(64 * NW, PP <= 128 ? NW / 2 : NW / 4) void lin_walk
     const float *gh = sg[c % kGateChunks][0], *gl = sg[c % kGateChunks][1];
     const float* in_w = sg[c % kGateChunks][REV ? 3 : 2];
     const float* up_w = sg[c % kGateChunks][REV ? 2 : 3];
-    if (!OUT && a.seg_decay != nullptr) seg_sum += (double)gh[CH - 1] + (double)gl[CH - 1];
+    if constexpr (!OUT) seg_sum += (double)sw_[c % kGateChunks][0] + (double)sw_[c % kGateChunks][1];
 
     f32x4 o[IT];
     if constexpr (OUT) {
@@ -166,6 +183,7 @@ __global__ __launch_bounds__(64 * NW, PP <= 128 ? NW / 2 : NW / 4) void lin_walk
         const int hi = wave < 2 ? 1 : 0, lo = wave == 1 ? 1 : 0, ti = REV ? lo : hi, tj = REV ? hi : lo;
         const int i = ti * 16 + l16;
         f32x4 acc = zero4(), bcc = zero4();
+        const uint32_t bad = sbad[c % kGateChunks];
 #pragma unroll
         for (int s = 0; s < PS; ++s) acc = mma(row_stk(sy + (tj * 16 + l16) * LY, s * 32), row_nat(sx + i * LX, s * 32), acc);
         if constexpr (DOT && !REV) {
@@ -183,6 +201,16 @@ __global__ __launch_bounds__(64 * NW, PP <= 128 ? NW / 2 : NW / 4) void lin_walk
           m[e] = j < i ? p[e] * bcc[e] : 0.f;
         }
         store_n<T, 4>(sp_ + i * LP + stacked(tj * 16 + 4 * g4), p, 4, true);
+        if (__builtin_expect(__builtin_amdgcn_readfirstlane((int)bad) != 0, 0)) {
+          int b_lane = lane;
+          asm volatile("" : "+v"(b_lane) : : "memory");  // as in Stage, and behind the store
+#pragma unroll 1
+          for (int e = 0; e < 4; ++e) {
+            const int bi = ti * 16 + b_lane % 16, bj = tj * 16 + b_lane / 16 * 4 + e, from = min(bi, bj), to = max(bi, bj);
+            if ((REV ? bj >= bi : bj <= bi) && (bad & ((2u << to) - (2u << from))) != 0)
+              sp_[bi * LP + stacked(bj)] = (T)__builtin_nanf("");
+          }
+        }
         if constexpr (DOT && !REV) {
           const float over = add_xor32(add_xor16((m[0] + m[1]) + (m[2] + m[3])));
           float (*t)[16] = sm[ti * IT + tj];
@@ -225,7 +253,7 @@ __global__ __launch_bounds__(64 * NW, PP <= 128 ? NW / 2 : NW / 4) void lin_walk
       __syncthreads();  // the pairs are there
     }
     // the state and, with the same columns of z, what the pairs give
-    const float dec = exp2_hw(gh[CH - 1]);
+    const float dec = sdec[c % kGateChunks];
 #pragma unroll
     for (int pt = 0; pt < PT; ++pt) S[pt] *= dec;
     bool careful = false;
