@@ -74,7 +74,9 @@ kda_status lin_check(const kda_lattn_dims* d, bool launching, LinPlan* p) {
   // rows of the outputs, in tiles whose offsets are held in 32 bits
   if ((int64_t)d->HV * std::max(d->K, d->V) > kMaxTileRow)
     return fail(KDA_EINVAL, "HV times K or V must be at most %lld", (long long)kMaxTileRow);
-  const int64_t cols = std::max<int64_t>(p->tiles, (d->V + p->tile_v - 1) / p->tile_v), slices = kda::lin_scan_slices((int64_t)d->K * d->V, p->slice);
+  // a walk's workgroups, counted by 256 threads: four a column of the tile
+  const int64_t cols = std::max<int64_t>(p->tiles * (p->tile_k / 64), (d->V + p->tile_v - 1) / p->tile_v * (p->tile_v / 64)),
+                slices = kda::lin_scan_slices((int64_t)d->K * d->V, p->slice);
   if (p->nseg * d->HV * cols > kMaxBlocks || (int64_t)d->N * d->HV * slices > kMaxBlocks)
     return fail(KDA_EINVAL, "too many segments (%lld of %d heads)", (long long)p->nseg, d->HV);
   return KDA_OK;

@@ -1,8 +1,12 @@
 """Sizes and limits of the token mixers' calls, as the library answers them (no GPU)."""
+import ctypes
 import subprocess
 import sys
 
 import pytest
+
+from chunked_gated_delta_09_amd import mixers
+from tests.test_mixers_host import lin_bwd, lin_dims, lin_fwd, refused
 
 FIRST_QUERY = """
 import ctypes
@@ -26,3 +30,16 @@ def test_the_first_query_of_a_process_answers_past_32_bits(lin, query):
     # a state of every sequence's; do.o of every row and one part of the queries at the least
     least = 2200 * 32 * 128 * 128 * 4 if lin else (1 << 22) * 255 * 4 + 1024 * 2 * 256 * 4 * 10
     assert int(r.stdout) >= least > 1 << 32
+
+
+@pytest.mark.parametrize("K,V", [(8, 128), (128, 8)])
+def test_grids_of_512_threads(K, V):
+    """Tiles of 128 columns have workgroups of 512 threads: 2^23 of them are more threads than a launch takes."""
+    lib = mixers._lib()
+    d = lin_dims(B=2100, N=2100, T=1, H=1 << 12, HV=1 << 12, K=K, V=V)
+    refused(lin_fwd(d), -1, "too many segments")
+    refused(lin_bwd(d), -1, "too many segments")
+    assert lib.kda_lattn_num_states(ctypes.byref(d)) == -1
+    assert lib.kda_lattn_bwd_workspace_bytes(ctypes.byref(d)) == 0
+    d.K, d.V = 8, 64
+    assert lib.kda_lattn_num_states(ctypes.byref(d)) == 2 * 2100  # of 256 threads each
