@@ -74,11 +74,16 @@ kda_status lin_check(const kda_lattn_dims* d, bool launching, LinPlan* p) {
   // rows of the outputs, in tiles whose offsets are held in 32 bits
   if ((int64_t)d->HV * std::max(d->K, d->V) > kMaxTileRow)
     return fail(KDA_EINVAL, "HV times K or V must be at most %lld", (long long)kMaxTileRow);
-  // a walk's workgroups, counted by 256 threads: four a column of the tile
-  const int64_t cols = std::max<int64_t>(p->tiles * (p->tile_k / 64), (d->V + p->tile_v - 1) / p->tile_v * (p->tile_v / 64)),
-                slices = kda::lin_scan_slices((int64_t)d->K * d->V, p->slice);
-  if (p->nseg * d->HV * cols > kMaxBlocks || (int64_t)d->N * d->HV * slices > kMaxBlocks)
-    return fail(KDA_EINVAL, "too many segments (%lld of %d heads)", (long long)p->nseg, d->HV);
+  return KDA_OK;
+}
+
+// The grids of a call over whole sequences: its walks' workgroups, counted by 256 threads (four a column of the tile), and
+// with `scan` the segments' scan's.
+kda_status lin_grids(const kda_lattn_dims* d, const LinPlan& p, bool bwd, bool scan) {
+  const int64_t cols_v = (d->V + p.tile_v - 1) / p.tile_v * (p.tile_v / 64), cols_k = p.tiles * (p.tile_k / 64);
+  const int64_t cols = bwd ? std::max(cols_k, cols_v) : cols_v, slices = scan ? kda::lin_scan_slices((int64_t)d->K * d->V, p.slice) : 0;
+  if (p.nseg * d->HV * cols > kMaxBlocks || (int64_t)d->N * d->HV * slices > kMaxBlocks)
+    return fail(KDA_EINVAL, "too many segments (%lld of %d sequences and %d heads)", (long long)p.nseg, d->N, d->HV);
   return KDA_OK;
 }
 
@@ -156,19 +161,19 @@ void lin_rows(kda::LinArgs* a, int dtype, int P, int R, const Rows& x, const Row
 
 KDA_EXPORT int64_t kda_lattn_num_states(const kda_lattn_dims* dims) {
   LinPlan p;
-  if (lin_check(dims, false, &p) != KDA_OK) return -1;
+  if (lin_check(dims, false, &p) != KDA_OK || lin_grids(dims, p, true, p.split) != KDA_OK) return -1;
   return p.nseg + dims->N;
 }
 
 KDA_EXPORT size_t kda_lattn_fwd_workspace_bytes(const kda_lattn_dims* dims) {
   LinPlan p;
-  if (lin_check(dims, false, &p) != KDA_OK) return 0;
+  if (lin_check(dims, false, &p) != KDA_OK || lin_grids(dims, p, false, p.split) != KDA_OK) return 0;
   return lin_layout(dims, p, false).total;
 }
 
 KDA_EXPORT size_t kda_lattn_bwd_workspace_bytes(const kda_lattn_dims* dims) {
   LinPlan p;
-  if (lin_check(dims, false, &p) != KDA_OK) return 0;
+  if (lin_check(dims, false, &p) != KDA_OK || lin_grids(dims, p, true, p.split) != KDA_OK) return 0;
   return lin_layout(dims, p, true).total;
 }
 
@@ -177,6 +182,7 @@ KDA_EXPORT kda_status kda_lattn_fwd(const kda_lattn_dims* dims, const void* q, c
                                     void* workspace, size_t ws_bytes, void* stream) {
   LinPlan p;
   TRY(lin_check(dims, true, &p));
+  TRY(lin_grids(dims, p, false, p.split));
   if (p.t.sq.total > 0) {
     REQUIRE(q, "q");
     REQUIRE(k, "k");
@@ -236,6 +242,8 @@ KDA_EXPORT kda_status kda_lattn_bwd(const kda_lattn_dims* dims, const void* q, c
                                     size_t ws_bytes, void* stream) {
   LinPlan p;
   TRY(lin_check(dims, true, &p));
+  const bool ends = p.split || dfinal != nullptr;  // some segment has a gradient at its end
+  TRY(lin_grids(dims, p, true, ends));
   REQUIRE(states, "states");
   if (p.t.sq.total > 0 || dims->g_const) REQUIRE(dg, "dg");
   if (p.t.sq.total > 0) {
@@ -279,7 +287,6 @@ KDA_EXPORT kda_status kda_lattn_bwd(const kda_lattn_dims* dims, const void* q, c
     b.seg_decay = reinterpret_cast<float*>(ws + l.decay);
     TRY(hip_status(kda::launch_lin_walk(dt, kda::kLinStateRev, b, st), "kda_lattn_bwd"));
   }
-  const bool ends = p.split || dfinal != nullptr;  // some segment has a gradient at its end
   if (ends) {
     kda::LinScanArgs s{};
     s.sq = p.t.sq;

@@ -6,7 +6,7 @@ import sys
 import pytest
 
 from chunked_gated_delta_09_amd import mixers
-from tests.test_mixers_host import lin_bwd, lin_dims, lin_fwd, refused
+from tests.test_mixers_host import P, lin_bwd, lin_dims, lin_fwd, packed, refused
 
 FIRST_QUERY = """
 import ctypes
@@ -37,9 +37,33 @@ def test_grids_of_512_threads(K, V):
     """Tiles of 128 columns have workgroups of 512 threads: 2^23 of them are more threads than a launch takes."""
     lib = mixers._lib()
     d = lin_dims(B=2100, N=2100, T=1, H=1 << 12, HV=1 << 12, K=K, V=V)
-    refused(lin_fwd(d), -1, "too many segments")
+    if V > 64:  # the forward has tiles of V alone
+        refused(lin_fwd(d), -1, "too many segments")
     refused(lin_bwd(d), -1, "too many segments")
     assert lib.kda_lattn_num_states(ctypes.byref(d)) == -1
     assert lib.kda_lattn_bwd_workspace_bytes(ctypes.byref(d)) == 0
     d.K, d.V = 8, 64
     assert lib.kda_lattn_num_states(ctypes.byref(d)) == 2 * 2100  # of 256 threads each
+
+
+def test_linear_limits_are_of_what_is_launched():
+    """The segments' scan is for sequences that are cut, and in the backward for gradients of final states."""
+    lib = mixers._lib()
+    d = lin_dims(B=40000, N=40000, T=1, H=32, HV=32, K=128, V=128)  # the scan would have 20 million workgroups
+    assert lib.kda_lattn_num_states(ctypes.byref(d)) == 2 * 40000
+    assert lib.kda_lattn_fwd_workspace_bytes(ctypes.byref(d)) == 0 and lib.kda_lattn_bwd_workspace_bytes(ctypes.byref(d)) > 0
+    refused(lin_fwd(d, *[None if i == 5 else P for i in range(8)]), -1, "o is NULL")
+    refused(lin_bwd(d, nulls={6, 7}), -1, "dq is NULL")
+    refused(lin_bwd(d), -1, "too many segments")
+    cu = list(range(40000)) + [50000]  # the last one is cut
+    host = packed(d, cu)
+    refused(lin_fwd(d), -1, "too many segments")
+    refused(lin_bwd(d, nulls={6}), -1, "too many segments")
+    assert lib.kda_lattn_num_states(ctypes.byref(d)) == -1
+    del host
+
+
+@pytest.mark.parametrize("B,HV,K,V", [(8192, 32, 256, 256), (32768, 32, 128, 128), (65535, 256, 64, 64)])
+def test_linear_steps_have_no_limit_of_whole_sequences(B, HV, K, V):
+    d = lin_dims(B=B, N=B, T=1, H=HV, HV=HV, K=K, V=V)
+    refused(mixers._lib().kda_lattn_step(ctypes.byref(d), P, P, P, P, P, 4, P, None, None), -1, "o is NULL")
