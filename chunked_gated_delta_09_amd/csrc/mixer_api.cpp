@@ -389,9 +389,6 @@ kda_status win_check(const kda_wattn_dims* d, bool launching, Tokens* t, kda::Wi
   TRY(tile_row(d->q_row, (int64_t)d->H * d->D, "q", &a->q_row));
   TRY(tile_row(d->k_row, (int64_t)d->HK * d->D, "k", &a->k_row));
   TRY(tile_row(d->v_row, (int64_t)d->HK * d->D, "v", &a->v_row));
-  if ((t->sq.total / 64 + d->N) * d->H > kMaxBlocks ||
-      (int64_t)d->N * d->sinks * d->HK > kMaxBlocks || (t->sq.total / 64 + d->N) * ((d->sinks + 15) / 16) * d->HK > kMaxBlocks)
-    return fail(KDA_EINVAL, "too many tokens (%lld of %d heads)", (long long)t->sq.total, d->H);
   a->sq = t->sq;
   a->H = d->H;
   a->HK = d->HK;
@@ -399,6 +396,12 @@ kda_status win_check(const kda_wattn_dims* d, bool launching, Tokens* t, kda::Wi
   a->window = d->window;
   a->sinks = d->sinks;
   a->scale = d->scale;
+  return KDA_OK;
+}
+
+// The grids over whole sequences: runs of 64 tokens at the least.
+kda_status win_grids(const kda_wattn_dims* d, const Tokens& t) {
+  if ((t.sq.total / 64 + d->N) * d->H > kMaxBlocks) return fail(KDA_EINVAL, "too many tokens (%lld of %d heads)", (long long)t.sq.total, d->H);
   return KDA_OK;
 }
 
@@ -433,6 +436,14 @@ WinLayout win_layout(const kda_wattn_dims* d, const Tokens& t) {
   return l;
 }
 
+// The backward's: also those of the first tokens where sequences are longer than the window.
+kda_status win_bwd_grids(const kda_wattn_dims* d, const Tokens& t, const WinLayout& l) {
+  TRY(win_grids(d, t));
+  if (l.parts > 0 && ((int64_t)d->N * d->sinks * d->HK > kMaxBlocks || l.parts * ((d->sinks + 15) / 16) * d->HK > kMaxBlocks))
+    return fail(KDA_EINVAL, "too many first tokens (%d of %d sequences and %d key heads)", d->sinks, d->N, d->HK);
+  return KDA_OK;
+}
+
 struct StepPlan {
   int rows, splits;
   size_t bytes;
@@ -457,6 +468,7 @@ KDA_EXPORT kda_status kda_wattn_fwd(const kda_wattn_dims* dims, const void* q, c
   Tokens t;
   kda::WinArgs a;
   TRY(win_check(dims, true, &t, &a));
+  TRY(win_grids(dims, t));
   if (t.sq.total > 0) {
     REQUIRE(q, "q");
     REQUIRE(k, "k");
@@ -486,7 +498,8 @@ KDA_EXPORT size_t kda_wattn_bwd_workspace_bytes(const kda_wattn_dims* dims) {
   Tokens t;
   kda::WinArgs a;
   if (win_check(dims, false, &t, &a) != KDA_OK) return 0;
-  return win_layout(dims, t).total;
+  const WinLayout l = win_layout(dims, t);
+  return win_bwd_grids(dims, t, l) == KDA_OK ? l.total : 0;
 }
 
 KDA_EXPORT kda_status kda_wattn_bwd(const kda_wattn_dims* dims, const void* q, const void* k, const void* v,
@@ -495,6 +508,8 @@ KDA_EXPORT kda_status kda_wattn_bwd(const kda_wattn_dims* dims, const void* q, c
   Tokens t;
   kda::WinArgs a;
   TRY(win_check(dims, true, &t, &a));
+  const WinLayout l = win_layout(dims, t);
+  TRY(win_bwd_grids(dims, t, l));
   if (t.sq.total == 0) return KDA_OK;
   REQUIRE(q, "q");
   REQUIRE(k, "k");
@@ -505,7 +520,6 @@ KDA_EXPORT kda_status kda_wattn_bwd(const kda_wattn_dims* dims, const void* q, c
   REQUIRE(dq, "dq");
   REQUIRE(dk, "dk");
   REQUIRE(dv, "dv");
-  const WinLayout l = win_layout(dims, t);
   TRY(check_ws(workspace, ws_bytes, l.total));
   char* ws = static_cast<char*>(workspace);
   a.q = q;
