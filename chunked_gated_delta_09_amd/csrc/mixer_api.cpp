@@ -456,7 +456,9 @@ kda_status win_step_check(const kda_wattn_dims* d, kda::WinArgs* c, StepPlan* p)
   const int total = d->sinks + d->window;
   p->rows = kda::win_step_rows(d->B, d->HK, total);
   p->splits = (total + p->rows - 1) / p->rows;
-  if ((int64_t)p->splits * d->H > kMaxBlocks) return fail(KDA_EINVAL, "too many heads (%d)", d->H);
+  // the step's workgroups (a row of sequences each) and, where a key head's rows are dealt to several, the join's
+  if ((int64_t)p->splits * d->H > kMaxBlocks || (p->splits > 1 && (int64_t)d->B * d->H > kMaxBlocks))
+    return fail(KDA_EINVAL, "too many heads (%d of %d sequences)", d->H, d->B);
   p->bytes = p->splits > 1 ? align_up((size_t)d->B * d->H * p->splits * (d->D + 2) * sizeof(float)) : 0;
   return KDA_OK;
 }

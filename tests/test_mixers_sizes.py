@@ -86,3 +86,16 @@ def test_window_steps_have_no_limit_of_whole_sequences(B, H, HK, sinks):
     d = win_dims(B=B, N=B, T=1, H=H, HK=HK, sinks=sinks)
     assert mixers._lib().kda_wattn_step_workspace_bytes(ctypes.byref(d)) == 0
     refused(win_step(d, nulls={7}), -1, "o is NULL")
+
+
+def test_the_join_of_a_window_step_has_its_own_limit():
+    """A workgroup for each head of each sequence, where a key head's cache rows are dealt to several."""
+    lib = mixers._lib()
+    d = win_dims(B=500, N=500, T=1, H=1 << 16, HK=1, D=8, window=1000)
+    refused(win_step(d, S=500), -1, "too many heads")
+    assert lib.kda_wattn_step_workspace_bytes(ctypes.byref(d)) == ctypes.c_size_t(-1).value
+    for change in (dict(window=100), dict(B=250, N=250)):  # one workgroup a key head; fewer than 2^24 of the join
+        for n, v in change.items():
+            setattr(d, n, v)
+        refused(win_step(d, S=500, nulls={7}), -1, "o is NULL")
+        d.window = 1000
