@@ -107,7 +107,8 @@ LinLayout lin_layout(const kda_lattn_dims* d, const LinPlan& p, bool bwd) {
     l.dots = o; o = align_up(o + (size_t)kda::lin_scan_slices((int64_t)d->K * d->V, p.slice) * p.nseg * d->HV * f);
     if (d->g_const) { l.part = o; o = align_up(o + (size_t)p.nseg * d->HV * sizeof(double)); }
     if (d->HV != d->H) {
-      l.dq = l.dk = o; o = align_up(o + rows * d->K * f);  // of one, then of the other
+      // dq's heads are summed before dk's are formed: kernels of one stream follow each other
+      l.dq = l.dk = o; o = align_up(o + rows * d->K * f);
     }
   }
   l.total = o;

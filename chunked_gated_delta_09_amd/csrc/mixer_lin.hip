@@ -48,7 +48,6 @@ hipError_t launch_lin_walk(int dtype, int mode, const LinArgs& args, hipStream_t
 
 namespace {
 
-
 // S_in of each segment from what the segments add: S <- decay S + added, elementwise over a state, in place. Backward, and
 // where the forward's states are given, also the products <dS, S> at the segments' ends.
 // E elements of a state a thread, the loads of AHEAD segments on their way together.
@@ -219,7 +218,7 @@ __global__ __launch_bounds__(64) void lin_gate_sum_kernel(const double* part, in
   if (threadIdx.x == 0) dg[hv] = (float)s;
 }
 
-// Sums over the rep heads of a group, of two arrays at once. VEC elements of a head a thread.
+// Sums over the rep heads of a group. VEC elements of a head a thread.
 template <class T, int VEC>
 __global__ __launch_bounds__(256) void group_sum_kernel(const float* in, T* out, int64_t n, int rep, int W) {
   for (int64_t i = (blockIdx.x * (int64_t)256 + threadIdx.x) * VEC; i < n; i += (int64_t)gridDim.x * 256 * VEC) {
