@@ -17,8 +17,8 @@ namespace kda {
 enum { kStateNone = 0, kStateSeq = 1, kStateSeg = 2, kStateStart = 3, kStateEnd = 4 };
 
 // Tokens of a chunk. Twice as many halve what is done once a chunk (the state's scaling and splitting, barriers), but each wave then
-// holds twice the rows of outputs and of the next chunk: 157, 159 us for the two walks without dot, where 32 take 140, 133 us
-// (B=4, T=4096, HV=32), and their tiles with w's leave room for one workgroup a CU.
+// holds twice the rows of outputs and of the next chunk: 157, 159 us for the two walks without dot, where 32 took 140, 133 us
+// (B=4, T=4096, HV=32; 120, 116 now), and their tiles with w's leave room for one workgroup a CU.
 constexpr int kLinChunk = 32;
 
 // What a walk over the chunks of a segment computes. Rows x, y [tokens, P] and z [tokens, R] of a head; state [P, R]:

@@ -28,7 +28,7 @@
 // sum_j M_ij - sum_j M_ji for each token from both products in fp32 (so a pair's two signs cancel exactly), and adds
 // q_i.dq_i of the state's part; the walk of dk gives k_i.dk_i of its state's part.
 //
-// Measured (B=4, T=4096, 32 value heads over 8 of 128 channels, bf16): states 71 us a pass, o 120, dv 125, dq 190, dk 176. Of dq's the
+// Measured (B=4, T=4096, 32 value heads over 8 of 128 channels, bf16): states 66 and 69 us, o 116, dv 120, dq 181, dk 171. Of dq's the
 // vector unit has work for 85 us (splitting, scaling, decays), the matrix unit for 45, shared memory for 52; they follow each other between
 // the chunk's barriers, with four waves a SIMD to fill the gaps. 372 MB read and 271 written take 125 us at the rate of a copy.
 #pragma once

@@ -15,8 +15,8 @@
 // Scores, statistics, P before its product, and all sums are fp32. P and dS are rounded to the type as operands (2^-9
 // relative each for bf16, as their outputs' own rounding).
 //
-// Measured, bf16: forward of a prompt of 16384 tokens, 16 heads of 128 channels, window 4096 610 us (780 TFLOP/s); training B=2, T=4096, 32
-// heads over 8, window 1024: forward 210, dq 276, dk and dv 383, first tokens 35 us. The vector unit (a score's scaling, exponential, maximum
+// Measured, bf16: forward of a prompt of 16384 tokens, 16 heads of 128 channels, window 4096 606 us (790 TFLOP/s); training B=2, T=4096, 32
+// heads over 8, window 1024: forward 208, dq 272, dk and dv 378, first tokens 35 us. The vector unit (a score's scaling, exponential, maximum
 // and sum) and the matrix unit have work for about a third of the time each, shared memory for 15 to 30 %; two waves a SIMD overlap them in part.
 #pragma once
 
