@@ -69,6 +69,22 @@ __device__ __forceinline__ void add_not_finite(const T* tile, int rows, f32x4 (&
           if (!(fabsf(x.at(e)) < INFINITY) && sees(n, r)) acc[d][n][e] += x.at(e);
     }
 }
+// Whether a wave's 32 rows hold something that is not finite.
+template <class T, int DP>
+__device__ __forceinline__ bool rows_not_finite(const T* tile) {
+  typedef Tile<T, DP> L;
+  constexpr int EV = 16 / (int)sizeof(T), PER = DP / EV;
+  float sum = 0.f;
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));  // as above
+#pragma unroll 1
+  for (int b = tid % 64; b < 32 * PER; b += 64) {
+    const auto x = load_n<T, EV>(tile + L::block(b / PER, b % PER), EV, true);
+#pragma unroll
+    for (int e = 0; e < EV; ++e) sum = fmaf(x.at(e), 0.f, sum);
+  }
+  return __any(!(sum == 0.f));
+}
 __device__ __forceinline__ bool any_not_finite(float sum) {
   return __builtin_amdgcn_readfirstlane(__syncthreads_or(!(sum == 0.f))) != 0;
 }
@@ -546,10 +562,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void win_
 
 // Sixteen keys: of the first ones over a part of the queries behind the window, or, where there are few keys, any over the
 // queries that see them through the window (NEAR). Each wave takes blocks of 32 queries of its own, through shared memory of
-// its own, and the waves' sums are joined at the end.
+// its own, and the waves' sums are joined at the end. Queries of a part that see none of the sixteen first tokens but through the
+// window are left out, or what is not finite in one that comes before a key would reach it (zero times an infinity). The others
+// come behind all sixteen, unless the window has less than 15 tokens and first tokens go on behind it: SHORT, which looks
+// at the blocks with such queries and forms them as the other kernels do.
 template <class T, int DP>
 constexpr int kKeysWaves = sizeof(T) * DP <= 512 ? 4 : 2;  // blocks of fp32 queries of 256 channels leave room for two
-template <class T, int DP, int NW, bool VEC, bool NEAR>
+template <class T, int DP, int NW, bool VEC, bool SHORT, bool NEAR>
 __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void win_keys_kernel(WinArgs a) {
   constexpr int DS = DP / 32, DT = DP / 16, EV = 16 / (int)sizeof(T), PER = DP / EV, N = 32 * PER / 64;
   typedef Tile<T, DP> L;
@@ -561,9 +580,9 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void 
   const int hk = (int)(blockIdx.x / per / ktiles);
   const Span sp = find_span(a.sq, NEAR ? 16 : a.part_len, (int)part, NEAR ? 0 : a.window);
   const int k0 = (NEAR ? sp.s : (int)(blockIdx.x / per % ktiles)) * 16;
-  const int qlo = NEAR ? k0 : a.window + sp.s * a.part_len;
-  const int qhi = NEAR ? (int)min((int64_t)sp.len, (int64_t)k0 + 15 + a.window) - 1 : min(qlo + a.part_len, sp.len) - 1;
-  if (qlo >= sp.len) return;  // a sequence without tokens, or no longer than the window
+  const int begin = NEAR ? k0 : a.window + sp.s * a.part_len, qlo = NEAR ? k0 : max(begin, k0 + a.window);
+  const int qhi = NEAR ? (int)min((int64_t)sp.len, (int64_t)k0 + 15 + a.window) - 1 : min(begin + a.part_len, sp.len) - 1;
+  if (begin >= sp.len) return;  // a sequence without tokens, or no longer than the window
   Frag<T> kf[DS], vf[DS];
   {
     const int j = k0 + l16;
@@ -578,7 +597,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void 
   }
   f32x4 dk[DT][1], dv[DT][1];
   const float scale2 = a.scale * kLog2e;
-  const int nb = (qhi - qlo) / 32 + 1;  // blocks of a head
+  const int nb = qhi < qlo ? 0 : (qhi - qlo) / 32 + 1;  // blocks of a head: none where the part ends before the tile's queries
   T *tq = sq[wave], *td = sd[wave];
   auto pass = [&](auto again) __attribute__((always_inline)) {
 #pragma unroll
@@ -622,6 +641,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void 
         }
       }
       wave_sync();
+      const bool careful = NEAR ? again.value && !(q0 >= k0 + 15 && q0 + 31 - k0 < a.window)
+                                : SHORT && q0 < k0 + 15 && (rows_not_finite<T, DP>(tq) || rows_not_finite<T, DP>(td));
       f32x4 s[2], dp[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -641,9 +662,6 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void 
         }
       }
       const Frag<T> pf = to_frag<T>(stack(s[0], s[1])), sf = to_frag<T>(stack(dp[0], dp[1]));
-      // a first token's key may come behind a query that is behind the window (more first tokens than the window has): such
-      // blocks are few, and formed without what is not finite at once
-      const bool careful = NEAR ? again.value && !(q0 >= k0 + 15 && q0 + 31 - k0 < a.window) : q0 < k0 + 15;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
         Frag<T> df = L::col(td, 0, dt * 16), qf = L::col(tq, 0, dt * 16);
@@ -655,8 +673,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void 
         dk[dt][0] = mma(qf, sf, dk[dt][0]);
       }
       if (careful) {
+        int c_tid = tid;
+        if constexpr (SHORT) asm volatile("" : "+v"(c_tid));  // as in add_not_finite
         auto seen = [&](int, int r) {
-          const int qi = q0 + r, j = k0 + l16;
+          const int qi = q0 + r, j = k0 + c_tid % 16;
           return NEAR ? j <= qi && qi - j < a.window : qi - j >= a.window;
         };
         add_not_finite<T, DP>(td, 32, dv, seen);
@@ -672,7 +692,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 && DP <= 128 ? 2 : 1) void 
       return false;
     }
   };
-  // of a pair that a part leaves out, but for those blocks, the query sees the key through the window
+  // of the pairs that a part leaves out, the query sees the key through the window, or the block has been looked at
   if (pass(std::false_type())) pass(std::true_type());
   // the waves' sums, in order
   constexpr int LO = 2 * DP + 4;
@@ -718,12 +738,16 @@ template <class T, int DP, int KT, int MODE>
 hipError_t win_dkv_t(const WinArgs& a, int krows, hipStream_t st) {
   constexpr int NW = kKeysWaves<T, DP>;
   if (krows == 16)
-    hipLaunchKernelGGL((win_keys_kernel<T, DP, NW, MODE != kOdd, true>), dim3((uint32_t)(a.blocks * a.HK)), dim3(64 * NW), 0, st, a);
+    hipLaunchKernelGGL((win_keys_kernel<T, DP, NW, MODE != kOdd, false, true>), dim3((uint32_t)(a.blocks * a.HK)), dim3(64 * NW), 0, st, a);
   else
     hipLaunchKernelGGL((win_dkv_kernel<T, DP, KT, MODE>), dim3((uint32_t)(a.blocks * a.HK)), dim3(256), 0, st, a);
   if (a.parts > 0) {
     const int64_t ktiles = (a.sinks + 15) / 16;
-    hipLaunchKernelGGL((win_keys_kernel<T, DP, NW, MODE != kOdd, false>), dim3((uint32_t)(a.parts * ktiles * a.HK)), dim3(64 * NW), 0, st, a);
+    const dim3 grid((uint32_t)(a.parts * ktiles * a.HK));
+    if (a.window < 15 && a.sinks > a.window)
+      hipLaunchKernelGGL((win_keys_kernel<T, DP, NW, MODE != kOdd, true, false>), grid, dim3(64 * NW), 0, st, a);
+    else
+      hipLaunchKernelGGL((win_keys_kernel<T, DP, NW, MODE != kOdd, false, false>), grid, dim3(64 * NW), 0, st, a);
   }
   return hipGetLastError();
 }

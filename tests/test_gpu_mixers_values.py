@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from tests.test_gpu_mixers import DT, lin_inputs, win_inputs
+from tests.test_gpu_mixers import DT, lin_inputs, win_check, win_inputs
 from tests.test_gpu_mixers_use import BAD, linear_all, poisoned, same, window_all
 
 pytestmark = pytest.mark.gpu
@@ -32,6 +32,32 @@ def test_more_first_tokens_than_the_window(dtype, window, sinks, n, H, HK, D, T)
             got = window_all(poisoned(dev, name, n, value, 1), window, sinks)
             for out in ("o", "dq"):
                 same(got[out], want[out], ~sees_n, name)
+
+
+@DT
+@pytest.mark.parametrize("window", [13, 14, 15, 16, 31, 33])
+@pytest.mark.parametrize("D,pad", [(128, 0), (100, 6), (256, 0), (16, 0)])
+def test_queries_just_behind_the_window(dtype, window, D, pad):
+    """Where the sixteen keys of a tile end among the queries of its first block."""
+    T, sinks = 300, 60
+    dev, _ = win_inputs(89, dtype, 1, T, 2, 1, D, pad)
+    want = window_all(dev, window, sinks)
+    t = torch.arange(T, device="cuda")
+    for n in (window, window + 1, 31, 32, 44, 45, 46, 47, 48):
+        seen = (t <= n) & ((n - t < window) | (t < sinks))
+        for name in ("q", "do"):
+            got = window_all(poisoned(dev, name, n, float("nan"), 1), window, sinks)
+            for out in ("dk", "dv"):
+                same(got[out], want[out], ~seen, (name, n))
+            assert not (got["dv"][0, seen, -1] if name == "q" else got["dv"][0, seen, -1, 1]).isfinite().any()
+
+
+@DT
+@pytest.mark.parametrize("window,sinks,cu", [(17, 1024, None), (5, 1024, [0, 600, 1500]), (14, 500, None), (100, 1000, [0, 120, 1500])])
+def test_parts_that_end_before_a_first_token(dtype, window, sinks, cu):
+    """First tokens beyond the first parts' queries."""
+    dev, x64 = win_inputs(91, dtype, 1, 1500, 4, 2, 40)
+    win_check(dev, x64, dtype, window, sinks, 0.2, cu, 1500, 40)
 
 
 @DT
