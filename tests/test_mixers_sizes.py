@@ -1,5 +1,6 @@
 """Sizes and limits of the token mixers' calls, as the library answers them (no GPU)."""
 import ctypes
+import os
 import subprocess
 import sys
 
@@ -25,7 +26,8 @@ print(plan.size("{query}"))
                                        (False, "kda_wattn_bwd_workspace_bytes")])
 def test_the_first_query_of_a_process_answers_past_32_bits(lin, query):
     """Nothing has declared the library's functions yet when a plan asks for a size."""
-    r = subprocess.run([sys.executable, "-c", FIRST_QUERY.format(lin=lin, query=query)], capture_output=True, text=True)
+    r = subprocess.run([sys.executable, "-c", FIRST_QUERY.format(lin=lin, query=query)], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0, r.stderr
     # a state of every sequence's; do.o of every row and one part of the queries at the least
     least = 2200 * 32 * 128 * 128 * 4 if lin else (1 << 22) * 255 * 4 + 1024 * 2 * 256 * 4 * 10
